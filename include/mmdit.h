@@ -475,6 +475,149 @@ MMDIT_API int mmdit_sparse_attn_table(const void* q, const void* k, const void* 
 MMDIT_API size_t mmdit_sparse_attn_table_workspace_size(const mmdit_tensor_desc* desc,
                                                         int max_blocks);
 
+/*
+ * Continuing a sequence (the digest's video extension and multi-shot clips:
+ * frames and audio tokens that attend to everything generated before them).
+ * The four calls below turn Q and K by their positions, keep K and V of the
+ * past in pages of 8-bit codes, attend to them, and copy pages.  Tensors of
+ * these calls are bf16 or f32 with head_dim 64 or 128, batch <= 65535.
+ */
+enum { MMDIT_PAIR_INTERLEAVED = 0, MMDIT_PAIR_HALF = 1 };
+enum { MMDIT_SCALE_NONE = 0, MMDIT_SCALE_LINEAR = 1, MMDIT_SCALE_NTK = 2, MMDIT_SCALE_PARTS = 3 };
+
+/* Rotary positions.  Channels form bands [t | h | w] of dim_t, dim_h, dim_w
+ * channels (each even, 2 <= sum <= head_dim); channels behind the bands pass
+ * unchanged, bit for bit.  Pair i of band b is (2i, 2i + 1) counted from the
+ * band start (INTERLEAVED) or (i, i + d_b/2) (HALF).  It turns by pos_b * w_i:
+ *   NONE    w_i = theta^(-2i/d_b)
+ *   LINEAR  w_i / f_b                              (positions pressed together)
+ *   NTK     theta replaced by theta f_b^(d_b/(d_b-2)) (the slowest pair as
+ *           under LINEAR, the fastest unchanged)
+ *   PARTS   g w_i + (1 - g) w_i / f_b, with
+ *           g = clamp((trained_b w_i / 2 pi - beta_slow)/(beta_fast - beta_slow), 0, 1):
+ *           pairs that turn often over the trained extent keep their frequency,
+ *           those that do not finish a turn are interpolated
+ * where f_b = factor[b] > 0 and trained[b] > 0 are the extension factor and the
+ * trained extent of the axis.  The turned pairs are multiplied by magnitude. */
+typedef struct {
+  double theta;
+  int32_t dim_t, dim_h, dim_w;
+  int32_t pairing;
+  int32_t scaling;
+  double factor[3], trained[3];  /* t, h, w; read by the scalings that use them */
+  double beta_fast, beta_slow;
+  double magnitude;              /* 1 for a plain rotation */
+} mmdit_rotary_params;
+
+/*
+ * mmdit_rotary -- q_out = R q and k_out = R k (transpose = 0), or R^T (1): the
+ *   gradient with respect to q and k given those of q_out and k_out.
+ *   q, k   : device [B, N, heads, head_dim]; either may be NULL (its output and
+ *            descriptors are then not read), not both.  They agree on B, N,
+ *            head_dim and dtype; heads and strides may differ.
+ *   q_out, k_out : same shapes, own strides; may be q or k itself (same
+ *            strides), and may not overlap any tensor of the call otherwise.
+ *   layout : the sequence that the tensors are a window of.
+ *   first  : NULL (0; the layout then holds at least N tokens) or device int32
+ *            [B]: token n of item b has the position of the layout's token
+ *            first[b] + n.  Indices outside the layout have position (0, 0, 0).
+ *   Angles are fp64 until their whole turns are removed; products are fp32.
+ *   Errors : EINVAL, EUNSUPPORTED, ECUDA.
+ */
+MMDIT_API int mmdit_rotary(const void* q, void* q_out, const mmdit_tensor_desc* q_desc,
+                           const mmdit_tensor_desc* q_out_desc, const void* k, void* k_out,
+                           const mmdit_tensor_desc* k_desc, const mmdit_tensor_desc* k_out_desc,
+                           const mmdit_layout* layout, const mmdit_rotary_params* params,
+                           const int32_t* first, int transpose, mmdit_stream_t stream);
+
+/* K and V of past tokens in pages.  Token n of item b lives in slot
+ * n % page_tokens of page page_table[b, n / page_tokens].  Codes are e4m3
+ * (4 exponent bits, bias 7, 3 mantissa bits; 0x7f and 0xff are NaN), device
+ * [n_pages, heads, page_tokens, head_dim] packed; a code stands for its e4m3
+ * value times the page's scale for that head. */
+typedef struct {
+  void* k;                    /* codes, 16-byte aligned */
+  void* v;
+  float* k_scale;             /* device float [n_pages, heads], each 0 or in 2^-60..2^60 */
+  float* v_scale;             /* (V scales of one item and head within 2^80 of one another) */
+  int32_t n_pages;
+  int32_t heads;              /* K/V heads */
+  int32_t page_tokens;        /* 16, 32, 64 or 128 */
+  int32_t head_dim;           /* 64 or 128 */
+  const int32_t* page_table;  /* device int32 [batch, max_pages]; unused by copy_pages */
+  int32_t batch;
+  int32_t max_pages;          /* pages per item: capacity max_pages * page_tokens tokens */
+} mmdit_cache;
+
+/*
+ * mmdit_cache_append -- stores K and V of tokens start[b] .. start[b] +
+ *   count[b] - 1 of every item.
+ *   k, v   : device [B, N, cache heads, head_dim] described by `desc`; token i
+ *            of item b becomes token start[b] + i
+ *   start  : device int32 [B]; tokens before start[b] are held already
+ *   count  : NULL (N everywhere) or device int32 [B], clamped to 0..N
+ *   layout, rotary : both NULL, or K is turned (as by mmdit_rotary with first =
+ *            start, in fp32, rounded only to its code) on the way in
+ *   The scale of a (page, head) is the power of two s with max|x| / s in
+ *   (224, 448] over the finite values stored in it, and >= 2^-60.  In a page that holds
+ *   older tokens of the item it is at least the scale that is there (rounded up
+ *   to a power of two); when it grows the older tokens' codes are rounded again.  Values become the nearest
+ *   e4m3 value of x / s (ties to even).  A token with an infinity or NaN among
+ *   its K or V values of a head keeps NaN codes for all of its K there, and zeros in
+ *   place of such values of V: rows that attend to it give NaN, and no others.
+ *   Every other slot of every page stays as it was.  Tokens at positions
+ *   outside 0 .. capacity - 1, or whose page id is outside 0 .. n_pages - 1, are not
+ *   stored.  No two items may append to the same page in one call.
+ *   Errors : EINVAL, EUNSUPPORTED, ECUDA.
+ */
+MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tensor_desc* desc,
+                                 const mmdit_cache* cache, const int32_t* start,
+                                 const int32_t* count, const mmdit_layout* layout,
+                                 const mmdit_rotary_params* rotary, mmdit_stream_t stream);
+
+/*
+ * mmdit_cache_attn -- o = softmax(q K^T * scale) V over the cached tokens.
+ *   q, o   : device [B, N, heads, head_dim], one dtype, own strides; heads is a
+ *            multiple g of the cache's heads, and query head h reads K/V head
+ *            h / g.  o may not alias q.
+ *   kv_len : device int32 [B]: tokens held per item, clamped to 0..capacity
+ *   q_len  : NULL (N) or device int32 [B], clamped to 0..N: the rows of o and
+ *            lse behind it are left as they were
+ *   causal_block : 0: every row sees all kv_len[b] tokens.  c >= 1: row i sits
+ *            at position p = kv_len[b] - q_len[b] + i and sees tokens below
+ *            (floor(p / c) + 1) c, i.e. its own block of c tokens (a frame; 1:
+ *            itself) and the blocks before it; rows at p < 0 see nothing.
+ *   scale  : > 0
+ *   lse    : NULL or device float [B, heads, N]: natural-log sum of exp
+ *   A row that sees no token has o = 0 and lse = -inf.  Tokens on a page whose id
+ *   is outside 0 .. n_pages - 1 are not seen.  Slots behind kv_len are never
+ *   used, whatever they hold.  Codes of V may not be NaN (the append writes
+ *   none).  Scores, softmax and sums are fp32.
+ *   workspace : mmdit_cache_attn_workspace_size bytes (0 is possible), 256-byte
+ *            aligned; partial results of split key ranges.  Two calls that may
+ *            run at the same time need one each.
+ *   Errors : EINVAL, EUNSUPPORTED, EWORKSPACE, ECUDA.
+ */
+MMDIT_API int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
+                               const mmdit_tensor_desc* o_desc, const mmdit_cache* cache,
+                               const int32_t* kv_len, const int32_t* q_len, int causal_block,
+                               float scale, float* lse, void* workspace, size_t ws_bytes,
+                               mmdit_stream_t stream);
+MMDIT_API size_t mmdit_cache_attn_workspace_size(const mmdit_tensor_desc* q_desc,
+                                                 const mmdit_cache* cache);
+
+/*
+ * mmdit_cache_copy_pages -- copies codes and scales of K and V of page src[i]
+ *   onto page dst[i], i < n: the tail page of a forked sequence (whole pages
+ *   are shared by listing their id in both page tables), or the pages that a
+ *   compaction moves into freed ids.
+ *   src, dst : host int32 [n], read during the call.  Ids in 0 .. n_pages - 1;
+ *              no id twice in dst, none in both lists (EINVAL otherwise).
+ *   Errors : EINVAL, EUNSUPPORTED, ECUDA.
+ */
+MMDIT_API int mmdit_cache_copy_pages(const mmdit_cache* cache, int n, const int32_t* src,
+                                     const int32_t* dst, mmdit_stream_t stream);
+
 /* Number of 4x4x4 blocks of the single BLOCK444 video segment of `layout`
  * (0 if the layout is not a single such segment). */
 MMDIT_API int mmdit_num_blocks(const mmdit_layout* layout);

@@ -31,11 +31,42 @@ struct RopeTab {
   int pt, ph, npairs;
 };
 
-// Position of token n of one batch item.  Video tokens in raster order:
-// (t0 + n / (H W), (n / W) % H, n % W).  Block-major (4x4x4) order: blocks in
-// (tb, hb, wb) raster order, tokens inside a block in (t, h, w) raster order
-// over the block's real extent.  Audio token j: (t0 + j t_num / t_den, 0, 0).
-// Text: (0, 0, 0).
+// Frame, row and column of token j of a video segment (before t0 is added):
+// raster order, (j / (H W), (j / W) % H, j % W), or block-major (4x4x4) order,
+// blocks in (tb, hb, wb) raster order, tokens inside a block in (t, h, w)
+// raster order over the block's real extent.
+__device__ __forceinline__ void video_coords(const DevSeg& g, int j, int& t, int& h, int& w) {
+  if (g.order == MMDIT_ORDER_RASTER) {
+    const int hw = g.H * g.W;
+    t = j / hw;
+    const int r = j - t * hw;
+    h = r / g.W;
+    w = r - h * g.W;
+  } else {
+    const int slab = 4 * g.H * g.W;
+    const int tb = j / slab;
+    int r = j - tb * slab;
+    const int et = min(4, g.T - 4 * tb);
+    const int row = et * 4 * g.W;
+    const int hb = r / row;
+    r -= hb * row;
+    const int eh = min(4, g.H - 4 * hb);
+    const int blk = et * eh * 4;
+    const int wb = r / blk;
+    r -= wb * blk;
+    const int ew = min(4, g.W - 4 * wb);
+    const int lt = r / (eh * ew);
+    r -= lt * eh * ew;
+    const int lh = r / ew;
+    const int lw = r - lh * ew;
+    t = 4 * tb + lt;
+    h = 4 * hb + lh;
+    w = 4 * wb + lw;
+  }
+}
+
+// Position of token n of one batch item.  Video tokens: (t0 + t, h, w) of
+// video_coords.  Audio token j: (t0 + j t_num / t_den, 0, 0).  Text: (0, 0, 0).
 __device__ __forceinline__ void token_position(const DevLayout& L, int n, float& pt,
                                                float& ph, float& pw) {
   pt = ph = pw = 0.f;
@@ -46,33 +77,7 @@ __device__ __forceinline__ void token_position(const DevLayout& L, int n, float&
     const int j = n - g.start;
     if (g.kind == MMDIT_SEG_VIDEO) {
       int t, h, w;
-      if (g.order == MMDIT_ORDER_RASTER) {
-        const int hw = g.H * g.W;
-        t = j / hw;
-        const int r = j - t * hw;
-        h = r / g.W;
-        w = r - h * g.W;
-      } else {
-        const int slab = 4 * g.H * g.W;
-        const int tb = j / slab;
-        int r = j - tb * slab;
-        const int et = min(4, g.T - 4 * tb);
-        const int row = et * 4 * g.W;
-        const int hb = r / row;
-        r -= hb * row;
-        const int eh = min(4, g.H - 4 * hb);
-        const int blk = et * eh * 4;
-        const int wb = r / blk;
-        r -= wb * blk;
-        const int ew = min(4, g.W - 4 * wb);
-        const int lt = r / (eh * ew);
-        r -= lt * eh * ew;
-        const int lh = r / ew;
-        const int lw = r - lh * ew;
-        t = 4 * tb + lt;
-        h = 4 * hb + lh;
-        w = 4 * wb + lw;
-      }
+      video_coords(g, j, t, h, w);
       pt = (float)(g.t0 + t);
       ph = (float)h;
       pw = (float)w;

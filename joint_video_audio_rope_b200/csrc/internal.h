@@ -189,5 +189,11 @@ int make_store_map(CUtensorMap* m, void* base, const mmdit_tensor_desc& d, int n
                    int cols, const char* name);
 int check_sm100();
 size_t align256(size_t x);
+DevLayout to_dev(const mmdit_layout* L);
+
+// paged 8-bit cache (cache.cu): descriptor checks of its calls and of
+// mmdit_rotary (bf16 or f32, head_dim 64 or 128, batch <= 65535)
+int check_cache_desc(const mmdit_tensor_desc* d, const char* name);
+int check_cache(const mmdit_cache* c, const char* name, bool table);
 
 }  // namespace mmdit

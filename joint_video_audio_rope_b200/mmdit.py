@@ -29,6 +29,8 @@ BF16, F32 = 0, 1
 SEG_VIDEO, SEG_AUDIO, SEG_TEXT = 0, 1, 2
 ORDER_RASTER, ORDER_BLOCK444 = 0, 1
 MAX_SEGMENTS = 8
+PAIR_INTERLEAVED, PAIR_HALF = 0, 1
+SCALE_NONE, SCALE_LINEAR, SCALE_NTK, SCALE_PARTS = range(4)
 
 
 class Segment(C.Structure):
@@ -55,10 +57,26 @@ class AdaptiveParams(C.Structure):
     _fields_ = [("tau_128", C.c_float), ("tau_256", C.c_float), ("eps", C.c_float)]
 
 
+class RotaryParams(C.Structure):
+    _fields_ = [("theta", C.c_double), ("dim_t", C.c_int32), ("dim_h", C.c_int32),
+                ("dim_w", C.c_int32), ("pairing", C.c_int32), ("scaling", C.c_int32),
+                ("factor", C.c_double * 3), ("trained", C.c_double * 3),
+                ("beta_fast", C.c_double), ("beta_slow", C.c_double), ("magnitude", C.c_double)]
+
+
+class Cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("n_pages", C.c_int32), ("heads", C.c_int32),
+                ("page_tokens", C.c_int32), ("head_dim", C.c_int32), ("page_table", C.c_void_p),
+                ("batch", C.c_int32), ("max_pages", C.c_int32)]
+
+
 _P = C.c_void_p
 _D = C.POINTER(TensorDesc)
 _L = C.POINTER(Layout)
 _R = C.POINTER(RopeParams)
+_RP = C.POINTER(RotaryParams)
+_C = C.POINTER(Cache)
 _SIGS = {
     "mmdit_rope_apply": (C.c_int, [_P, _P, _D, _L, _R, _P]),
     "mmdit_joint_attn": (C.c_int, [_P, _P, _P, _P, _P, _D, _L, C.c_float, _R, _P, C.c_int64,
@@ -102,6 +120,13 @@ _SIGS = {
     "mmdit_sparse_attn_table": (C.c_int, [_P, _P, _P, _P, _D, _P, _P, C.c_int, _P, _P, C.c_int,
                                           C.c_float, _P, C.c_size_t, _P]),
     "mmdit_sparse_attn_table_workspace_size": (C.c_size_t, [_D, C.c_int]),
+    "mmdit_rotary": (C.c_int, [_P, _P, _D, _D, _P, _P, _D, _D, _L, _RP, _P, C.c_int, _P]),
+    "mmdit_cache_append": (C.c_int, [_P, _P, _D, _C, _P, _P, _L, _RP, _P]),
+    "mmdit_cache_attn": (C.c_int, [_P, _P, _D, _D, _C, _P, _P, C.c_int, C.c_float, _P, _P,
+                                   C.c_size_t, _P]),
+    "mmdit_cache_attn_workspace_size": (C.c_size_t, [_D, _C]),
+    "mmdit_cache_copy_pages": (C.c_int, [_C, C.c_int, C.POINTER(C.c_int32), C.POINTER(C.c_int32),
+                                         _P]),
     "mmdit_device_status": (C.c_int, [_P]),
     "mmdit_selftest_wait_timeout": (C.c_int, [C.c_int, _P, _P]),
     "mmdit_last_error": (C.c_char_p, []),
@@ -387,6 +412,79 @@ def sparse_attn_table(q, k, v, o, desc: TensorDesc, blocks, n_blocks, max_blocks
 
 def sparse_attn_table_workspace_size(desc: TensorDesc, max_blocks: int) -> int:
     return _lib.mmdit_sparse_attn_table_workspace_size(C.byref(desc), max_blocks)
+
+
+def rotary_params(theta: float, dim_t: int, dim_h: int = 0, dim_w: int = 0,
+                  pairing: int = PAIR_INTERLEAVED, scaling: int = SCALE_NONE,
+                  factors=(1.0, 1.0, 1.0), trained=(0.0, 0.0, 0.0), beta_fast: float = 32.0,
+                  beta_slow: float = 1.0, magnitude: float = 1.0) -> RotaryParams:
+    """Parameters of mmdit_rotary; factors and trained per axis (t, h, w)."""
+    f3 = C.c_double * 3
+    return RotaryParams(theta, dim_t, dim_h, dim_w, pairing, scaling, f3(*factors), f3(*trained),
+                        beta_fast, beta_slow, magnitude)
+
+
+def rotary(q, q_out, q_desc, q_out_desc, k, k_out, k_desc, k_out_desc, layout: Layout,
+           params: RotaryParams, first=None, transpose: bool = False, stream=None) -> None:
+    """q_out = R q and k_out = R k (transpose: R^T, the gradient) at the positions of the
+    layout's tokens first[b] + n; q or k may be None with its three companions."""
+    _check(_lib.mmdit_rotary(_ptr(q), _ptr(q_out), _ref(q_desc), _ref(q_out_desc), _ptr(k),
+                             _ptr(k_out), _ref(k_desc), _ref(k_out_desc), C.byref(layout),
+                             C.byref(params), _ptr(first), 1 if transpose else 0,
+                             _stream(stream)))
+
+
+def make_cache(k, v, k_scale, v_scale, page_table=None) -> Cache:
+    """Handle of a paged cache: codes [n_pages, heads, page_tokens, head_dim] of an 8-bit
+    dtype, scales float [n_pages, heads], page_table int32 [batch, max_pages] (None for calls that
+    take no tokens).  Holds addresses: keep the tensors alive."""
+    import torch
+    if k.dim() != 4 or k.shape != v.shape or k.element_size() != 1 or v.element_size() != 1:
+        raise ValueError("expected 8-bit codes [n_pages, heads, page_tokens, head_dim] for k and v")
+    if any(x.shape != k.shape[:2] or x.dtype != torch.float32 for x in (k_scale, v_scale)):
+        raise ValueError("expected float32 scales [n_pages, heads]")
+    if not all(x.is_contiguous() for x in (k, v, k_scale, v_scale)):
+        raise ValueError("the arrays of a cache are packed")
+    batch = per = 0
+    if page_table is not None:
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous():
+            raise ValueError("expected a packed int32 page table [batch, max_pages]")
+        batch, per = page_table.shape
+    return Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1],
+                 k.shape[2], k.shape[3], _ptr(page_table), batch, per)
+
+
+def cache_append(k, v, desc: TensorDesc, cache: Cache, start, count=None,
+                 layout: Optional[Layout] = None, rotation: Optional[RotaryParams] = None,
+                 stream=None) -> None:
+    """Stores tokens start[b] .. start[b] + count[b] - 1 (int32 [B] on the device; count None:
+    all N) in 8 bits; with layout and rotation, K is turned on the way."""
+    _check(_lib.mmdit_cache_append(_ptr(k), _ptr(v), C.byref(desc), C.byref(cache), _ptr(start),
+                                   _ptr(count), _ref(layout), _ref(rotation), _stream(stream)))
+
+
+def cache_attn_workspace_size(q_desc: TensorDesc, cache: Cache) -> int:
+    return _lib.mmdit_cache_attn_workspace_size(C.byref(q_desc), C.byref(cache))
+
+
+def cache_attn(q, o, q_desc: TensorDesc, o_desc: TensorDesc, cache: Cache, kv_len, scale: float,
+               q_len=None, causal_block: int = 0, lse=None, workspace=None, ws_bytes: int = 0,
+               stream=None) -> None:
+    """o = softmax(q K^T * scale) V over the first kv_len[b] cached tokens (int32 [B] on the
+    device); causal_block = c: a row sees its own and earlier blocks of c tokens.  Workspace from
+    cache_attn_workspace_size."""
+    _check(_lib.mmdit_cache_attn(_ptr(q), _ptr(o), C.byref(q_desc), C.byref(o_desc),
+                                 C.byref(cache), _ptr(kv_len), _ptr(q_len), causal_block, scale,
+                                 _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def cache_copy_pages(cache: Cache, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
+    """Copies pages src[i] onto pages dst[i] (codes and scales of K and V)."""
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError("src and dst differ in length")
+    ids = C.c_int32 * max(n, 1)
+    _check(_lib.mmdit_cache_copy_pages(C.byref(cache), n, ids(*src), ids(*dst), _stream(stream)))
 
 
 def num_blocks(layout: Layout) -> int:
