@@ -19,8 +19,6 @@
 // are the probabilities of an fp32 call.  The next slab's loads are in flight
 // while the current one is computed.  Each warp runs its own softmax; the CTA's
 // warps, then the key ranges, are merged at the end in a fixed order.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
@@ -32,20 +30,12 @@ namespace mmdit {
 namespace {
 
 constexpr int kFewWarps = 4;
-constexpr int kUnit = 128;  // tokens: granularity of the split key ranges
+// bf16 rows per (item, K/V head) up to which 16-row tiles are taken
+constexpr int kFewRows = 64;
 // The largest probability of a row is held as 2^14: fp16 keeps its relative
 // precision down to 2^-14, so what is 2^-28 of the largest is still whole.
 constexpr float kShift = 14.f;
 
-__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {  // two e4m3 codes
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float2 unpack_half2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
@@ -56,13 +46,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// 2^k that brings |x| <= amax to at most 2^15 (1 where amax is 0, infinite or NaN).
-__device__ __forceinline__ float fit_half(float amax) {
-  if (!(amax > 0.f && amax <= 3.402823466e38f)) return 1.f;
-  const int e = (__float_as_int(amax) >> 23) - 127;  // amax < 2^(e+1)
-  return __int_as_float((min(max(14 - e, -126), 126) + 127) << 23);
 }
 
 template <typename T>
@@ -93,15 +76,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.z, tiles = A.rows / kFewTile;
-  const int hk = blockIdx.x / tiles, r0 = (blockIdx.x % tiles) * kFewTile;
-  const int kv = held_tokens(A, b), ql = query_tokens(A, b);
-  const int live = min(kFewTile, ql * A.G - r0);  // rows of this tile that exist
+  const CacheItem w = item_of(A, blockIdx.x, kFewTile);
+  const int b = w.b, hk = w.hk, r0 = w.r0, kv = w.kv, ql = w.ql, live = w.live;
+  const int lo = w.lo, hi = w.hi;
   if (live <= 0) return;
-  const int kmax = visible_keys(A, kv, ql, (r0 + live - 1) / A.G);
-  const int units = (kmax + kUnit - 1) / kUnit, per = (units + A.splits - 1) / A.splits;
-  const int lo = min(kmax, (int)blockIdx.y * per * kUnit);
-  const int hi = min(kmax, lo + per * kUnit);
 
   // ---- Q fragments of rows g and g + 8, and the rows' visible keys
   uint32_t qa[QP][KK][4];
@@ -343,26 +321,26 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   if (row >= live) return;
   float M = -INFINITY, L = 0.f, out[W];
 #pragma unroll
-  for (int w = 0; w < kFewWarps; ++w) M = fmaxf(M, sm_ml[w][row][0]);
+  for (int x = 0; x < kFewWarps; ++x) M = fmaxf(M, sm_ml[x][row][0]);
   const float Mr = M == -INFINITY ? 0.f : M;
 #pragma unroll
   for (int c = 0; c < W; ++c) out[c] = 0.f;
 #pragma unroll
-  for (int w = 0; w < kFewWarps; ++w) {
-    const float f = ex2_approx(sm_ml[w][row][0] - Mr);
-    L = fmaf(f, sm_ml[w][row][1], L);
+  for (int x = 0; x < kFewWarps; ++x) {
+    const float f = ex2_approx(sm_ml[x][row][0] - Mr);
+    L = fmaf(f, sm_ml[x][row][1], L);
 #pragma unroll
     for (int c = 0; c < W; c += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&sm_o[w][row][c0 + c * TPR]);
-      out[c] = fmaf(f, x.x, out[c]);
-      out[c + 1] = fmaf(f, x.y, out[c + 1]);
-      out[c + 2] = fmaf(f, x.z, out[c + 2]);
-      out[c + 3] = fmaf(f, x.w, out[c + 3]);
+      const float4 y = *reinterpret_cast<const float4*>(&sm_o[x][row][c0 + c * TPR]);
+      out[c] = fmaf(f, y.x, out[c]);
+      out[c + 1] = fmaf(f, y.y, out[c + 1]);
+      out[c + 2] = fmaf(f, y.z, out[c + 2]);
+      out[c + 3] = fmaf(f, y.w, out[c + 3]);
     }
   }
   const int r = r0 + row;
-  if (A.splits > 1) {
-    const long long pr = (((long long)blockIdx.y * A.B + b) * A.Hk + hk) * A.rows + r;
+  if (w.part >= 0) {
+    const long long pr = w.part * kFewTile + row;
 #pragma unroll
     for (int c = 0; c < W; c += 4)
       *reinterpret_cast<float4*>(A.part_o + pr * D + c0 + c * TPR) =
@@ -391,20 +369,22 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
-// Merges the key ranges of one row in their order: a warp per (item, token,
-// head), a lane for D / 32 channels.
+// Merges the key ranges of the split items in their order: a warp per row, a
+// lane for D / 32 channels.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-    cache_attn_merge_kernel(const __grid_constant__ CacheAttnArgs A) {
+    cache_attn_merge_kernel(const __grid_constant__ CacheAttnArgs A, int tile) {
   constexpr int W = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= (long long)A.B * A.N * A.H) return;
-  const int head = (int)(i % A.H), tok = (int)(i / A.H % A.N), b = (int)(i / A.H / A.N);
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);  // over the split items' rows
+  const int item = i / tile, row = i % tile;
+  int b, hk, r0;
+  item_rows(A, A.whole + item, tile, b, hk, r0);
+  if (b >= A.B) return;
+  const int r = r0 + row, tok = r / A.G, head = hk * A.G + r % A.G;
   if (tok >= query_tokens(A, b)) return;
-  const int hk = head / A.G, r = tok * A.G + head % A.G;
-  const long long step = (long long)A.B * A.Hk * A.rows;
-  const long long p0 = ((long long)b * A.Hk + hk) * A.rows + r;
+  const long long step = tile;
+  const long long p0 = (long long)item * A.splits * tile + row;
   float M = -INFINITY;
   for (int s = lane; s < A.splits; s += 32) M = fmaxf(M, A.part_ml[2 * (p0 + s * step)]);
 #pragma unroll
@@ -440,25 +420,45 @@ __global__ void __launch_bounds__(256)
         L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
-// Rows per tile, key ranges and workspace of a call, from what the host knows
+// Kernel, items, key ranges and workspace of a call, from what the host knows
 // (the lengths are on the device: a range of an item is cut there, from its
 // own length).
 struct CachePlan {
-  int rows, splits;
+  int tile, tiles;  // rows per item, row tiles per (item, K/V head)
+  long long items, whole;
+  int splits;
   size_t part_o_bytes, bytes;
+  long long grid() const { return whole + (items - whole) * splits; }
 };
 
 CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
   CachePlan p{};
   const long long rows = (long long)q.n_tokens * (q.heads / c.heads);
-  p.rows = (int)((rows + kFewTile - 1) / kFewTile * kFewTile);
-  // Two CTAs of four warps per SM keep enough loads in flight; a range is at
-  // least 512 tokens (16 slabs for the CTA), or its merge costs more than it saves.
-  const long long ctas = std::max(1LL, (long long)p.rows / kFewTile * c.heads * q.batch);
   const long long cap = (long long)c.max_pages * c.page_tokens;
-  p.splits = (int)std::max(1LL, std::min(2 * 148 / ctas, (cap + 511) / 512));
-  if (p.splits > 1) {
-    const size_t n = (size_t)p.splits * q.batch * c.heads * p.rows;
+  p.tile = q.dtype == MMDIT_BF16 && rows > kFewRows ? kManyTile : kFewTile;
+  p.tiles = (int)((rows + p.tile - 1) / p.tile);
+  p.items = (long long)p.tiles * c.heads * q.batch;
+  if (p.tile == kFewTile) {
+    // Two CTAs of four warps per SM keep enough loads in flight; a range is at
+    // least 512 tokens (16 slabs for the CTA), or its merge costs more than it saves.
+    p.splits = (int)std::max(1LL, std::min(2 * 148 / p.items, (cap + 511) / 512));
+    p.whole = p.splits > 1 ? 0 : p.items;
+  } else {
+    // One CTA per SM.  What is left behind the whole waves is split so that its
+    // waves are short: ceil(left s / 148) waves of the key tiles of a range and about
+    // four more for its set-up and its merge.
+    p.whole = p.items / 148 * 148;
+    p.splits = 1;
+    const long long left = p.items - p.whole, units = (cap + kUnit - 1) / kUnit;
+    long long best = 0;
+    for (int s = 1; s <= std::min(148LL, std::max(1LL, units / 4)); ++s) {
+      const long long cost = (left * s + 147) / 148 * ((units + s - 1) / s + (s > 1 ? 4 : 0));
+      if (s == 1 || cost < best) best = cost, p.splits = s;
+    }
+    if (p.splits == 1) p.whole = p.items;
+  }
+  const size_t n = (size_t)(p.items - p.whole) * p.splits * p.tile;
+  if (n > 0) {
     p.part_o_bytes = align256(n * q.head_dim * sizeof(float));
     p.bytes = p.part_o_bytes + align256(n * 2 * sizeof(float));
   }
@@ -466,16 +466,22 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
 }
 
 template <typename T, int D>
-cudaError_t launch_few(const CacheAttnArgs& A, cudaStream_t s) {
-  const dim3 grid(A.Hk * (A.rows / kFewTile), A.splits, A.B);
-  cache_attn_few_kernel<T, D><<<grid, kFewWarps * 32, 0, s>>>(A);
+cudaError_t launch_few(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
+  cache_attn_few_kernel<T, D><<<(unsigned)p.grid(), kFewWarps * 32, 0, s>>>(A);
   return cudaGetLastError();
 }
 template <typename T, int D>
-cudaError_t launch_merge(const CacheAttnArgs& A, cudaStream_t s) {
-  const long long rows = (long long)A.B * A.N * A.H;
-  cache_attn_merge_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(A);
+cudaError_t launch_merge(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
+  const long long rows = (p.items - p.whole) * p.tile;
+  cache_attn_merge_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(A, p.tile);
   return cudaGetLastError();
+}
+template <typename T, int D>
+cudaError_t launch_cache_attn(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
+  cudaError_t e = p.tile == kManyTile ? launch_cache_attn_many(A, D, (unsigned)p.grid(), s)
+                                      : launch_few<T, D>(A, p, s);
+  if (e == cudaSuccess && p.whole < p.items) e = launch_merge<T, D>(A, p, s);
+  return e;
 }
 
 int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c) {
@@ -486,20 +492,13 @@ int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c) {
     return fail(MMDIT_EINVAL, "cache_attn: q and cache disagree on batch or head_dim");
   if (q->heads % c->heads != 0)
     return fail(MMDIT_EINVAL, "cache_attn: %d query heads over %d K/V heads", q->heads, c->heads);
-  const long long rows = (long long)q->n_tokens * (q->heads / c->heads) + 256;
-  if (rows / kFewTile * c->heads > 0x7fffffffLL || rows > 0x7fffffffLL ||
-      (long long)q->batch * q->n_tokens * q->heads > (0x7fffffffLL - 8) * 8)
+  const long long rows = (long long)q->n_tokens * (q->heads / c->heads) + kManyTile;
+  if (rows > 0x7fffffffLL || (rows / kFewTile + 1) * c->heads * q->batch > 0x7fffffffLL)
     return fail(MMDIT_EINVAL, "cache_attn: too many query rows");
   return MMDIT_OK;
 }
 
 }  // namespace
-
-cudaError_t launch_cache_attn_few(const CacheAttnArgs& A, int D, int dtype, cudaStream_t s) {
-  if (dtype == MMDIT_BF16)
-    return D == 128 ? launch_few<__nv_bfloat16, 128>(A, s) : launch_few<__nv_bfloat16, 64>(A, s);
-  return D == 128 ? launch_few<float, 128>(A, s) : launch_few<float, 64>(A, s);
-}
 
 }  // namespace mmdit
 
@@ -564,7 +563,8 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   A.G = A.H / A.Hk;
   A.causal = causal_block;
   A.scale_log2 = scale * 1.4426950408889634f;
-  A.rows = plan.rows;
+  A.tiles = plan.tiles;
+  A.whole = (int)plan.whole;
   A.splits = plan.splits;
   A.part_o = (float*)workspace;
   A.part_ml = (float*)((char*)workspace + plan.part_o_bytes);
@@ -572,13 +572,12 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
     return fail(MMDIT_ECUDA, "device error flag unavailable");
   cudaStream_t s = (cudaStream_t)stream;
   const int D = q_desc->head_dim;
-  cudaError_t e = launch_cache_attn_few(A, D, q_desc->dtype, s);
-  if (e == cudaSuccess && A.splits > 1) {
-    if (q_desc->dtype == MMDIT_BF16)
-      e = D == 128 ? launch_merge<__nv_bfloat16, 128>(A, s) : launch_merge<__nv_bfloat16, 64>(A, s);
-    else
-      e = D == 128 ? launch_merge<float, 128>(A, s) : launch_merge<float, 64>(A, s);
-  }
+  cudaError_t e;
+  if (q_desc->dtype == MMDIT_BF16)
+    e = D == 128 ? launch_cache_attn<__nv_bfloat16, 128>(A, plan, s)
+                 : launch_cache_attn<__nv_bfloat16, 64>(A, plan, s);
+  else
+    e = D == 128 ? launch_cache_attn<float, 128>(A, plan, s) : launch_cache_attn<float, 64>(A, plan, s);
   return e == cudaSuccess ? MMDIT_OK : cuda_fail(e, "cache_attn launch");
 }
 

@@ -12,6 +12,9 @@
 // result needs no pass over V's values.
 #pragma once
 
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "internal.h"
 
 namespace mmdit {
@@ -27,13 +30,19 @@ struct CacheAttnArgs {
   int n_pages, page, max_pages;
   int B, N, H, Hk, G;  // G = H / Hk
   int causal;
-  int splits;          // key ranges per row tile; > 1: partial results
   float scale_log2;
-  float* part_o;       // [splits][B][Hk][rows][D], unnormalised
-  float* part_ml;      // [splits][B][Hk][rows][2]: maximum (log2) and sum
-  int rows;            // N * G rounded up to whole row tiles
+  // Items: one tile of rows of one (item, K/V head).  The first `whole` of them
+  // are one CTA each; each of the others is split into `splits` key ranges.
+  int tiles;           // row tiles per (item, K/V head)
+  int whole, splits;
+  float* part_o;       // [item - whole][split][tile rows][D], unnormalised
+  float* part_ml;      // [item - whole][split][tile rows][2]: maximum (log2) and sum
   int* err;
 };
+
+constexpr int kFewTile = 16;    // rows per CTA: few rows, and every fp32 call (cache_attn.cu)
+constexpr int kManyTile = 256;  // many bf16 rows, on tcgen05 (cache_attn_tc.cu)
+constexpr int kUnit = 128;      // tokens: granularity of the split key ranges
 
 __device__ __forceinline__ int held_tokens(const CacheAttnArgs& A, int b) {
   return min(max(A.kv_len[b], 0), A.max_pages * A.page);
@@ -56,8 +65,64 @@ __device__ __forceinline__ int page_of(const CacheAttnArgs& A, int b, int n) {
   return (id >= 0 && id < A.n_pages) ? id : -1;
 }
 
-// few query rows (cache_attn.cu); many bf16 rows on tcgen05 (cache_attn_tc.cu)
-constexpr int kFewTile = 16;
-cudaError_t launch_cache_attn_few(const CacheAttnArgs& A, int D, int dtype, cudaStream_t s);
+
+// What one CTA works on.
+struct CacheItem {
+  int b, hk, r0, live;  // rows r0 .. r0 + live - 1
+  int kv, ql;
+  int lo, hi;           // key range
+  long long part;       // partial result, or -1: the item is whole
+};
+// Row tiles from the last to the first: with causal_block the last ones see the
+// most keys, and the longest items are best started first.
+__device__ __forceinline__ void item_rows(const CacheAttnArgs& A, int i, int tile, int& b, int& hk,
+                                          int& r0) {
+  r0 = (A.tiles - 1 - i % A.tiles) * tile;
+  i /= A.tiles;
+  hk = i % A.Hk;
+  b = i / A.Hk;
+}
+__device__ __forceinline__ CacheItem item_of(const CacheAttnArgs& A, int i, int tile) {
+  CacheItem w;
+  int split = 0, splits = 1;
+  w.part = -1;
+  if (i >= A.whole) {
+    w.part = i - A.whole;
+    splits = A.splits;
+    split = (i - A.whole) % splits;
+    i = A.whole + (i - A.whole) / splits;
+  }
+  item_rows(A, i, tile, w.b, w.hk, w.r0);
+  w.kv = held_tokens(A, w.b);
+  w.ql = query_tokens(A, w.b);
+  w.live = min(tile, w.ql * A.G - w.r0);
+  w.lo = w.hi = 0;
+  if (w.live > 0) {
+    const int keys = visible_keys(A, w.kv, w.ql, (w.r0 + w.live - 1) / A.G);
+    const int units = (keys + kUnit - 1) / kUnit, per = (units + splits - 1) / splits;
+    w.lo = min(keys, split * per * kUnit);
+    w.hi = min(keys, w.lo + per * kUnit);
+  }
+  return w;
+}
+
+// 2^k that brings |x| <= amax to at most 2^15 (1 where amax is 0, infinite or NaN).
+__device__ __forceinline__ float fit_half(float amax) {
+  if (!(amax > 0.f && amax <= 3.402823466e38f)) return 1.f;
+  const int e = (__float_as_int(amax) >> 23) - 127;  // amax < 2^(e+1)
+  return __int_as_float((min(max(14 - e, -126), 126) + 127) << 23);
+}
+__device__ __forceinline__ uint32_t half2_of(uint32_t codes) {  // two e4m3 codes
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// bf16 q; `grid` CTAs (cache_attn_tc.cu)
+cudaError_t launch_cache_attn_many(const CacheAttnArgs& A, int D, unsigned grid, cudaStream_t s);
 
 }  // namespace mmdit

@@ -1,0 +1,503 @@
+// mmdit_cache_attn for many bf16 query rows: tcgen05 tiles over the paged cache.
+//
+// A CTA (512 threads, one per SM) takes 256 query rows of one K/V head (two
+// tiles of 128) and a range of its keys:
+//   warps 0-3, 4-7  softmax of row tile 0 and 1 (thread = row)
+//   warps 8-11      converters: codes from global memory to registers, one
+//                   tile ahead of use, and as fp16 (e4m3 is exact there) into
+//                   the swizzled K and V tiles
+//   warp 12         one thread issues the MMAs
+// Tensor memory: [0,128) S0 / P0, [128,256) S1 / P1, then O0 and O1 (D columns each).
+//
+// S = Q K^T with Q as fp16: each row is multiplied by the power of two that puts
+// its largest value at 2^14..2^15 (bf16 is exact there down to 2^-29 of it).
+// With f = Q's factor^-1 * scale * log2(e) * (K scale), constant over the 16
+// tokens of a page group, the exponent is t = S f + log2(V scale): its row
+// maximum is found group by group from the maxima of S, so the scales cost eight
+// multiply-adds per row and tile.  P = 2^(t - m + 7) is held as fp16; m follows the
+// maximum only once it has grown by 2^8 (P <= 2^15 then), and terms down to 2^-32
+// of the largest are still held.  The sum of weights adds up 2^(t - m + 7) / (V scale) per
+// group.
+#include <math.h>
+
+#include "cache_attn.cuh"
+
+namespace mmdit {
+
+namespace {
+
+constexpr int kKeys = 128;                // keys per tile
+constexpr int kHalf = 128 * 128;          // bytes of 64 channels of a 128-row fp16 tile
+constexpr int kThreads = 512;
+constexpr int kScaleSlots = 4;            // tiles whose scales are held
+constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
+constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
+// registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
+constexpr int kRegsSoftmax = 192, kRegsConvert = 88, kRegsMma = 40;
+static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 512, "register split");
+
+template <int D>
+struct Many {
+  static constexpr int kTile = 128 * D * 2;  // bytes of a 128-row fp16 tile
+  static constexpr int kKOff = 2 * kTile;    // behind the two Q tiles
+  static constexpr int kVOff = kKOff + 2 * kTile;
+  static constexpr int kScaleOff = kVOff + 2 * kTile;              // float4 [slots][8]
+  static constexpr int kMulOff = kScaleOff + kScaleSlots * 8 * 16;  // float [256]
+  static constexpr int kBarOff = kMulOff + 256 * 4;
+  static constexpr int kSmem = kBarOff + 256 + 1024;  // and room to align
+  static constexpr uint32_t kIdescQK = (1u << 4) | (kKeys / 8 << 17) | (128 / 16 << 24);
+  static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (D / 8 << 17) | (128 / 16 << 24);
+};
+
+enum {
+  M_QREADY = 0,  // 2: Q tile written (128 arrivals)
+  M_KFULL = 2,   // 2: K tile converted (128)
+  M_KEMPTY = 4,  // 2: its QKs done (commit)
+  M_VFULL = 6,
+  M_VEMPTY = 8,
+  M_SCALES = 10,  // 4: scales of a tile written (128)
+  M_SFULL = 14,   // 2: S in tensor memory (commit)
+  M_PHALF = 16,   // 2: P of keys 0..63 written (128)
+  M_PFULL = 18,   // 2: P written (128)
+  M_OFULL = 20,   // 2: last PV done (commit)
+  M_DONE = 22,    // 1: every MMA done (commit)
+  M_COUNT = 23
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    cache_attn_many_kernel(const __grid_constant__ CacheAttnArgs A) {
+  using C = Many<D>;
+  const CacheItem w = item_of(A, blockIdx.x, kManyTile);
+  if (w.live <= 0) return;
+  const int tiles = (w.hi - w.lo + kKeys - 1) / kKeys;  // 0: nothing to see
+  const int nt = w.live > 128 ? 2 : 1;                  // row tiles in use
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * M_COUNT);
+  float4* scales = reinterpret_cast<float4*>(smem + C::kScaleOff);
+  float* muls = reinterpret_cast<float*>(smem + C::kMulOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* err = A.err;
+  const bool skip = *(volatile int*)err != 0;  // an earlier kernel timed out
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(M_QREADY + t), 128);
+      mbar_init(bar(M_KFULL + t), 128);
+      mbar_init(bar(M_KEMPTY + t), 1);
+      mbar_init(bar(M_VFULL + t), 128);
+      mbar_init(bar(M_VEMPTY + t), 1);
+      mbar_init(bar(M_SFULL + t), 1);
+      mbar_init(bar(M_PHALF + t), 128);
+      mbar_init(bar(M_PFULL + t), 128);
+      mbar_init(bar(M_OFULL + t), 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(M_SCALES + i), 128);
+    mbar_init(bar(M_DONE), 1);
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issuer
+    // As P_t lies over S_t, tile t's order is QK(0), PV(0), QK(1), PV(1), ...;
+    // the two row tiles alternate, so one's softmax runs under the other's MMAs.
+    setmaxnreg_dec<kRegsMma>();
+    if (warp == 12 && lane == 0 && !skip) {
+      bool ok = true;
+      auto qk = [&](int t, int slot) {
+        const uint64_t a = smem_desc_sw128(sbase + t * C::kTile, 16, 1024);
+        const uint64_t b = smem_desc_sw128(sbase + C::kKOff + slot * C::kTile, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t at = (uint64_t)((k >> 2) * (kHalf >> 4) + (k & 3) * 2);
+          tc_mma_ss(tmem + t * 128, a + at, b + at, C::kIdescQK, k > 0);
+        }
+        tc_commit(bar(M_SFULL + t));
+      };
+      auto pv = [&](int t, int slot, int half, bool add) {
+        const uint64_t b = smem_desc_sw128(sbase + C::kVOff + slot * C::kTile, kHalf, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_ts(tmem + 256 + t * D, tmem + t * 128 + (4 * half + k) * 8,
+                    b + (uint64_t)((4 * half + k) * 128), C::kIdescPV, add || half + k > 0);
+      };
+      if (tiles > 0) {
+        for (int t = 0; t < nt && ok; ++t) ok = mbar_wait(bar(M_QREADY + t), 0, err);
+        ok = ok && mbar_wait(bar(M_KFULL), 0, err);
+        if (ok) {
+          tc_fence_after();
+          for (int t = 0; t < nt; ++t) qk(t, 0);
+          tc_commit(bar(M_KEMPTY));
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int sv = j & 1, sk = sv ^ 1;
+          const bool more = j + 1 < tiles;
+          if (!(ok = mbar_wait(bar(M_VFULL + sv), (j >> 1) & 1, err))) break;
+          for (int t = 0; t < nt; ++t) {
+            if (!(ok = mbar_wait(bar(M_PHALF + t), j & 1, err))) break;
+            tc_fence_after();
+            pv(t, sv, 0, j > 0);
+            if (!(ok = mbar_wait(bar(M_PFULL + t), j & 1, err))) break;
+            tc_fence_after();
+            pv(t, sv, 1, true);
+            if (t == nt - 1) tc_commit(bar(M_VEMPTY + sv));
+            if (more) {
+              if (t == 0 && !(ok = mbar_wait(bar(M_KFULL + sk), ((j + 1) >> 1) & 1, err))) break;
+              tc_fence_after();
+              qk(t, sk);
+              if (t == nt - 1) tc_commit(bar(M_KEMPTY + sk));
+            }
+          }
+        }
+      }
+      for (int t = 0; t < nt; ++t) tc_commit(bar(M_OFULL + t));
+      tc_commit(bar(M_DONE));
+      mbar_wait(bar(M_DONE), 0, err);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ converters
+    // A warp converts 32 tokens of each tile.  Eight lanes hold four 16-code
+    // vectors of two neighbouring tokens: their fp16 chunks fall on all eight
+    // 16-byte columns of the swizzled tile, so the stores meet no bank twice.
+    setmaxnreg_dec<kRegsConvert>();
+    constexpr int NI = D / 16;                   // vectors per thread and tile
+    constexpr int RS = 32 / NI;                  // tokens per load instruction
+    const int cw = warp - 8;
+    const int c4 = lane & 3, half = D == 128 ? (lane >> 3) & 1 : 0;
+    const int row = ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
+    const long long head_bytes = (long long)A.page * D;
+    const int at = half * 64 + c4 * 16;
+    int id[2], id2[2];
+    float ks[2], vs[2], ks2[2], vs2[2];
+    auto find = [&](int j, int (&p)[2], float (&k)[2], float (&v)[2]) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int n = w.lo + j * kKeys + cw * 32 + f * 16;
+        p[f] = n < w.hi ? page_of(A, w.b, n) : -1;
+        k[f] = v[f] = 0.f;
+        if (p[f] >= 0) {
+          k[f] = __ldg(A.k_scale + (long long)p[f] * A.Hk + w.hk);
+          v[f] = __ldg(A.v_scale + (long long)p[f] * A.Hk + w.hk);
+        }
+      }
+    };
+    auto load = [&](const uint8_t* codes, int j, const int (&p)[2], uint4 (&r)[NI]) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int f = i * RS >= 16, tok = w.lo + j * kKeys + cw * 32 + i * RS + row;
+        r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p[f] >= 0 && tok < w.hi)
+          r[i] = __ldg(reinterpret_cast<const uint4*>(
+              codes + ((long long)p[f] * A.Hk + w.hk) * head_bytes + (tok & (A.page - 1)) * D + at));
+      }
+    };
+    auto store = [&](uint8_t* tile, const uint4 (&r)[NI]) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int n = cw * 32 + i * RS + row;
+        uint8_t* line = tile + half * kHalf + n * 128;
+        uint4 a, b;
+        a.x = half2_of(r[i].x & 0xffffu), a.y = half2_of(r[i].x >> 16);
+        a.z = half2_of(r[i].y & 0xffffu), a.w = half2_of(r[i].y >> 16);
+        b.x = half2_of(r[i].z & 0xffffu), b.y = half2_of(r[i].z >> 16);
+        b.z = half2_of(r[i].w & 0xffffu), b.w = half2_of(r[i].w >> 16);
+        *reinterpret_cast<uint4*>(line + (((2 * c4) ^ (n & 7)) << 4)) = a;
+        *reinterpret_cast<uint4*>(line + (((2 * c4 + 1) ^ (n & 7)) << 4)) = b;
+      }
+    };
+    uint4 kr[NI], vr[NI];
+    if (tiles > 0) {
+      find(0, id, ks, vs);
+      load(A.k, 0, id, kr);
+      load(A.v, 0, id, vr);
+    }
+    bool ok = !skip;
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int slot = j & 1;
+      const uint32_t free = ((j >> 1) & 1) ^ 1;
+      const bool more = j + 1 < tiles;
+      if (more) find(j + 1, id2, ks2, vs2);
+      if (!(ok = mbar_wait(bar(M_KEMPTY + slot), free, err))) break;
+      if ((lane & 15) == 0) {
+        // a page that is not there is not seen; a V scale of 0 stands for zeros
+        const int f = lane >> 4;
+        const float v = f ? vs[1] : vs[0];
+        scales[(j % kScaleSlots) * 8 + cw * 2 + f] =
+            make_float4(f ? ks[1] : ks[0],
+                        (f ? id[1] : id[0]) < 0 ? -INFINITY : (v > 0.f ? log2f(v) : 0.f),
+                        v > 0.f ? 1.f / v : 1.f, 0.f);
+      }
+      mbar_arrive(bar(M_SCALES + j % kScaleSlots));
+      store(smem + C::kKOff + slot * C::kTile, kr);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(M_KFULL + slot));
+      if (more) load(A.k, j + 1, id2, kr);
+      if (!(ok = mbar_wait(bar(M_VEMPTY + slot), free, err))) break;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (!(vs[i * RS >= 16] > 0.f)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      store(smem + C::kVOff + slot * C::kTile, vr);
+      fence_proxy_async_smem();
+      mbar_arrive(bar(M_VFULL + slot));
+      if (more) load(A.v, j + 1, id2, vr);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) id[f] = id2[f], ks[f] = ks2[f], vs[f] = vs2[f];
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<kRegsSoftmax>();
+    const int t = warp >> 2;
+    const int row = threadIdx.x;  // 0 .. 255
+    const bool valid = row < w.live;
+    if (t < nt) {
+      if (tiles > 0) {
+        // Q rows of this warp: fp16, largest value at 2^14..2^15
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
+        const int c = lane % LPR;
+#pragma unroll 4
+        for (int i = 0; i < 32; i += RPI) {
+          const int n = warp * 32 + i + lane / LPR, r = w.r0 + n;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (n < w.live)
+            v = *reinterpret_cast<const uint4*>(
+                (const __nv_bfloat16*)A.q + w.b * A.q_sb + (long long)(r / A.G) * A.q_st +
+                (long long)(w.hk * A.G + r % A.G) * D + c * 8);
+          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
+          float2 x[4];
+          float am = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[k] = __bfloat1622float2(p[k]);
+            am = fmaxf(am, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+          }
+#pragma unroll
+          for (int off = LPR / 2; off > 0; off >>= 1)
+            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
+          const float f = fit_half(am);
+          v.x = pack_half2(x[0].x * f, x[0].y * f);
+          v.y = pack_half2(x[1].x * f, x[1].y * f);
+          v.z = pack_half2(x[2].x * f, x[2].y * f);
+          v.w = pack_half2(x[3].x * f, x[3].y * f);
+          *reinterpret_cast<uint4*>(smem + t * C::kTile + (c >> 3) * kHalf + (n & 127) * 128 +
+                                    (((c & 7) ^ (n & 7)) << 4)) = v;
+          if (c == 0) muls[n] = A.scale_log2 / f;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(M_QREADY + t));
+        __syncwarp();
+      }
+      const float mul = muls[row];
+      const int limit = valid ? visible_keys(A, w.kv, w.ql, (w.r0 + row) / A.G) : 0;
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t s_addr = tmem + lane_off + t * 128;
+      const uint32_t o_addr = tmem + lane_off + 256 + t * D;
+      float m = -INFINITY, l = 0.f;  // reference maximum of t, sum of weights
+      bool ok = !skip;
+      for (int j = 0; j < tiles; ++j) {
+        const int slot = j % kScaleSlots;
+        ok = ok && mbar_wait(bar(M_SCALES + slot), (j / kScaleSlots) & 1, err) &&
+             mbar_wait(bar(M_SFULL + t), j & 1, err);
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t v0[32], v1[32], v2[32], v3[32];
+          tmem_ld32(s_addr, v0);
+          tmem_ld32(s_addr + 32, v1);
+          tmem_ld32(s_addr + 64, v2);
+          tmem_ld32(s_addr + 96, v3);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            s[i] = __uint_as_float(v0[i]);
+            s[32 + i] = __uint_as_float(v1[i]);
+            s[64 + i] = __uint_as_float(v2[i]);
+            s[96 + i] = __uint_as_float(v3[i]);
+          }
+        }
+        const int lim = min(limit, w.hi) - (w.lo + j * kKeys);
+        if (lim < kKeys) {
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (i >= lim) s[i] = -INFINITY;
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float* x = s + 16 * g;
+          const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]), x[6]);
+          const float b = max3f(max3f(x[7], x[8], x[9]), max3f(x[10], x[11], x[12]), x[13]);
+          const float4 sc = scales[slot * 8 + g];
+          // at least the smallest normal number: -inf stays -inf
+          const float f = fmaxf(mul * sc.x, 1.1754944e-38f);
+          mt = fmaxf(mt, fmaf(max3f(a, b, fmaxf(x[14], x[15])), f, sc.y));
+        }
+        const bool grow = mt > m + kGrow || (m == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float alpha = grow ? ex2_approx(m - mt) : 1.f;
+          if (grow) m = mt;
+          l *= alpha;
+          // the PV before is complete: it was issued before this tile's QK
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t v[32];
+              tmem_ld32(o_addr + c * 32, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                v[i] = __float_as_uint(__uint_as_float(v[i]) * alpha);
+              tmem_st32(o_addr + c * 32, v);
+            }
+            tmem_wait_st();
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : kManyShift - m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 2 * c; g < 2 * c + 2; ++g) {
+            const float4 sc = scales[slot * 8 + g];
+            const float f = fmaxf(mul * sc.x, 1.1754944e-38f), d = sc.y + shift;
+            const uint64_t f2 = pack_f32x2(f, f), d2 = pack_f32x2(d, d);
+            uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float p0, p1;
+              unpack_f32x2(ffma_f32x2(pack_f32x2(s[16 * g + 2 * i], s[16 * g + 2 * i + 1]), f2, d2),
+                           p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              pk[(g & 1) * 8 + i] = pack_half2(p0, p1);
+              acc[i & 1] = add_f32x2(acc[i & 1], pack_f32x2(p0, p1));
+            }
+            float a0, a1;
+            unpack_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
+            l = fmaf(a0 + a1, sc.z, l);
+          }
+          tmem_st16(s_addr + c * 16, pk);
+          if (c == 1) {  // the first half of PV may start
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(M_PHALF + t));
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(M_PFULL + t));
+      }
+
+      // ---------------------------------------------------------- epilogue
+      ok = ok && mbar_wait(bar(M_OFULL + t), 0, err);
+      if (__all_sync(0xffffffffu, ok)) {
+        __syncwarp();
+        tc_fence_after();
+        const float mref = m == -INFINITY ? -INFINITY : m - kManyShift;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+        const int r = w.r0 + row, tok = r / A.G, head = w.hk * A.G + r % A.G;
+        const long long pr = w.part * kManyTile + row;
+        uint8_t* stage = smem + t * C::kTile + (warp & 3) * (32 * D * 2);  // Q's place
+        constexpr int CH = D / 8;  // 16-byte chunks per output row
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          if (tiles > 0) {
+            tmem_ld32(o_addr + c * 32, v);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0u;
+          }
+          if (w.part >= 0) {
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<uint4*>(A.part_o + pr * D + c * 32 + i) =
+                    make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint4 o;
+              o.x = pack_bf16x2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+              o.y = pack_bf16x2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+              o.z = pack_bf16x2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+              o.w = pack_bf16x2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+              const int chunk = c * 4 + i / 8;
+              *reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((chunk ^ (lane & 7)) << 4)) = o;
+            }
+          }
+        }
+        if (w.part >= 0) {
+          if (valid) *reinterpret_cast<float2*>(A.part_ml + 2 * pr) = make_float2(mref, l);
+        } else {
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 32; i += 32 / CH) {
+            const int n = i + lane / CH, chunk = lane % CH, rr = warp * 32 + n;
+            if (rr < w.live) {
+              const int q = w.r0 + rr;
+              *reinterpret_cast<uint4*>((__nv_bfloat16*)A.o + w.b * A.o_sb +
+                                        (long long)(q / A.G) * A.o_st +
+                                        (long long)(w.hk * A.G + q % A.G) * D + chunk * 8) =
+                  *reinterpret_cast<const uint4*>(stage + n * (D * 2) + ((chunk ^ (n & 7)) << 4));
+            }
+          }
+          if (A.lse && valid)
+            A.lse[((long long)w.b * A.H + head) * A.N + tok] =
+                l == 0.f ? -INFINITY : (mref + log2f(l)) * 0.69314718055994531f;
+        }
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_many(const CacheAttnArgs& A, unsigned grid, cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once_per_device(dev, [] {
+    return cudaFuncSetAttribute(cache_attn_many_kernel<D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cache_attn_many_kernel<D><<<grid, kThreads, Many<D>::kSmem, s>>>(A);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attn_many(const CacheAttnArgs& A, int D, unsigned grid, cudaStream_t s) {
+  return D == 128 ? launch_many<128>(A, grid, s) : launch_many<64>(A, grid, s);
+}
+
+}  // namespace mmdit
