@@ -33,7 +33,7 @@ constexpr int kScaleSlots = 4;            // tiles whose scales are held
 constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
 constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
 // registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
-constexpr int kRegsSoftmax = 192, kRegsConvert = 88, kRegsMma = 40;
+constexpr int kRegsSoftmax = 176, kRegsConvert = 96, kRegsMma = 64;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 512, "register split");
 
 template <int D>
@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nt = w.live > 128 ? 2 : 1;                  // row tiles in use
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  // an offset, not a cast address: the accesses below stay shared-memory ones
+  uint8_t* smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * M_COUNT);
@@ -179,30 +179,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - 8;
     const int c4 = lane & 3, half = D == 128 ? (lane >> 3) & 1 : 0;
     const int row = ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
-    const long long head_bytes = (long long)A.page * D;
-    const int at = half * 64 + c4 * 16;
-    int id[2], id2[2];
-    float ks[2], vs[2], ks2[2], vs2[2];
-    auto find = [&](int j, int (&p)[2], float (&k)[2], float (&v)[2]) {
+    const int gpp = A.page >> 4;  // 16-token groups per page
+    const int n0 = w.lo + cw * 32;
+    // pages of the warp's two groups in tile j; -1: nothing to load
+    auto find = [&](int j, int (&p)[2]) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const int n = w.lo + j * kKeys + cw * 32 + f * 16;
+        const int n = n0 + j * kKeys + f * 16;
         p[f] = n < w.hi ? page_of(A, w.b, n) : -1;
-        k[f] = v[f] = 0.f;
-        if (p[f] >= 0) {
-          k[f] = __ldg(A.k_scale + (long long)p[f] * A.Hk + w.hk);
-          v[f] = __ldg(A.v_scale + (long long)p[f] * A.Hk + w.hk);
-        }
       }
+    };
+    // this half warp's scales
+    auto find_scales = [&](const int (&p)[2], float& k, float& v) {
+      const int page = lane < 16 ? p[0] : p[1];
+      k = v = 0.f;
+      if (page >= 0) {
+        k = __ldg(A.k_scale + (long long)page * A.Hk + w.hk);
+        v = __ldg(A.v_scale + (long long)page * A.Hk + w.hk);
+      }
+    };
+    // Writes them for the softmax and returns which groups have a V scale.  A page
+    // that is not there is not seen; a V scale of 0 stands for zeros.
+    auto put_scales = [&](int j, const int (&p)[2], float k, float v) {
+      const int page = lane < 16 ? p[0] : p[1];
+      if ((lane & 15) == 0)
+        scales[(j % kScaleSlots) * 8 + cw * 2 + (lane >> 4)] =
+            make_float4(k, page < 0 ? -INFINITY : (v > 0.f ? log2f(v) : 0.f),
+                        v > 0.f ? 1.f / v : 1.f, 0.f);
+      mbar_arrive(bar(M_SCALES + j % kScaleSlots));
+      return __ballot_sync(0xffffffffu, v > 0.f);
     };
     auto load = [&](const uint8_t* codes, int j, const int (&p)[2], uint4 (&r)[NI]) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int f = i * RS >= 16, tok = w.lo + j * kKeys + cw * 32 + i * RS + row;
-        r[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (p[f] >= 0 && tok < w.hi)
-          r[i] = __ldg(reinterpret_cast<const uint4*>(
-              codes + ((long long)p[f] * A.Hk + w.hk) * head_bytes + (tok & (A.page - 1)) * D + at));
+      for (int f = 0; f < 2; ++f) {
+        const int n = n0 + j * kKeys + f * 16;
+        const uint8_t* src =
+            codes + (((long long)p[f] * A.Hk + w.hk) * gpp + ((n >> 4) & (gpp - 1))) * (16 * D) +
+            row * D + half * 64 + c4 * 16;
+        const int rows = p[f] >= 0 ? w.hi - n - row : 0;  // of this thread's tokens and later ones
+#pragma unroll
+        for (int i = 0; i < NI / 2; ++i) {
+          r[f * (NI / 2) + i] = make_uint4(0u, 0u, 0u, 0u);
+          if (i * RS < rows) r[f * (NI / 2) + i] = __ldg(reinterpret_cast<const uint4*>(src + i * RS * D));
+        }
       }
     };
     auto store = [&](uint8_t* tile, const uint4 (&r)[NI]) {
@@ -220,42 +239,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     uint4 kr[NI], vr[NI];
-    if (tiles > 0) {
-      find(0, id, ks, vs);
-      load(A.k, 0, id, kr);
-      load(A.v, 0, id, vr);
-    }
+    int pg[2], pg2[2];  // pages of the next tile and of the one behind it
+    float sk, sv;
+    uint32_t scaled = 0;
     bool ok = !skip;
+    if (tiles > 0) {
+      find(0, pg);
+      find(1, pg2);
+      find_scales(pg, sk, sv);
+      load(A.k, 0, pg, kr);
+      load(A.v, 0, pg, vr);
+      scaled = put_scales(0, pg, sk, sv);
+    }
     for (int j = 0; j < tiles && ok; ++j) {
       const int slot = j & 1;
       const uint32_t free = ((j >> 1) & 1) ^ 1;
       const bool more = j + 1 < tiles;
-      if (more) find(j + 1, id2, ks2, vs2);
-      if (!(ok = mbar_wait(bar(M_KEMPTY + slot), free, err))) break;
-      if ((lane & 15) == 0) {
-        // a page that is not there is not seen; a V scale of 0 stands for zeros
-        const int f = lane >> 4;
-        const float v = f ? vs[1] : vs[0];
-        scales[(j % kScaleSlots) * 8 + cw * 2 + f] =
-            make_float4(f ? ks[1] : ks[0],
-                        (f ? id[1] : id[0]) < 0 ? -INFINITY : (v > 0.f ? log2f(v) : 0.f),
-                        v > 0.f ? 1.f / v : 1.f, 0.f);
+      pg[0] = pg2[0], pg[1] = pg2[1];
+      if (more) {
+        find_scales(pg, sk, sv);
+        find(j + 2, pg2);
       }
-      mbar_arrive(bar(M_SCALES + j % kScaleSlots));
+      if (!(ok = mbar_wait(bar(M_KEMPTY + slot), free, err))) break;
       store(smem + C::kKOff + slot * C::kTile, kr);
       fence_proxy_async_smem();
       mbar_arrive(bar(M_KFULL + slot));
-      if (more) load(A.k, j + 1, id2, kr);
+      if (more) load(A.k, j + 1, pg, kr);
       if (!(ok = mbar_wait(bar(M_VEMPTY + slot), free, err))) break;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (!(vs[i * RS >= 16] > 0.f)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (!(scaled >> (i >= NI / 2 ? 16 : 0) & 1u)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
       store(smem + C::kVOff + slot * C::kTile, vr);
       fence_proxy_async_smem();
       mbar_arrive(bar(M_VFULL + slot));
-      if (more) load(A.v, j + 1, id2, vr);
-#pragma unroll
-      for (int f = 0; f < 2; ++f) id[f] = id2[f], ks[f] = ks2[f], vs[f] = vs2[f];
+      if (more) {
+        load(A.v, j + 1, pg, vr);
+        // the slot's last readers, the softmaxes of tile j - 3, are behind the QK of
+        // tile j - 2, which was waited for above
+        scaled = put_scales(j + 1, pg, sk, sv);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax
