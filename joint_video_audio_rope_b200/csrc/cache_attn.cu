@@ -555,6 +555,7 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   A.q_len = q_len;
   A.n_pages = cache->n_pages;
   A.page = cache->page_tokens;
+  while ((1 << A.page_log2) < A.page) ++A.page_log2;
   A.max_pages = cache->max_pages;
   A.B = q_desc->batch;
   A.N = q_desc->n_tokens;

@@ -27,7 +27,7 @@ struct CacheAttnArgs {
   const uint8_t *k, *v;
   const float *k_scale, *v_scale;
   const int32_t *table, *kv_len, *q_len;
-  int n_pages, page, max_pages;
+  int n_pages, page, page_log2, max_pages;
   int B, N, H, Hk, G;  // G = H / Hk
   int causal;
   float scale_log2;
@@ -60,7 +60,7 @@ __device__ __forceinline__ int visible_keys(const CacheAttnArgs& A, int kv, int 
 }
 // Page of token n of item b, or -1 (nothing to see there).
 __device__ __forceinline__ int page_of(const CacheAttnArgs& A, int b, int n) {
-  const int id = __ldg(A.table + (long long)b * A.max_pages + n / A.page);
+  const int id = __ldg(A.table + (long long)b * A.max_pages + (n >> A.page_log2));
   MMDIT_DCHECK(id >= 0 && id < A.n_pages, A.err);
   return (id >= 0 && id < A.n_pages) ? id : -1;
 }

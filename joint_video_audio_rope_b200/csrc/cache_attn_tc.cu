@@ -6,7 +6,8 @@
 //   warps 8-11      converters: codes from global memory to registers, one
 //                   tile ahead of use, and as fp16 (e4m3 is exact there) into
 //                   the swizzled K and V tiles
-//   warp 12         one thread issues the MMAs
+//   warp 12         issues the MMAs
+//   warp 13         looks up the pages and scales of the tiles to come
 // Tensor memory: [0,128) S0 / P0, [128,256) S1 / P1, then O0 and O1 (D columns each).
 //
 // S = Q K^T with Q as fp16: each row is multiplied by the power of two that puts
@@ -29,7 +30,7 @@ namespace {
 constexpr int kKeys = 128;                // keys per tile
 constexpr int kHalf = 128 * 128;          // bytes of 64 channels of a 128-row fp16 tile
 constexpr int kThreads = 512;
-constexpr int kScaleSlots = 4;            // tiles whose scales are held
+constexpr int kPageSlots = 8;             // tiles whose pages and scales are held
 constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
 constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
 // registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
@@ -41,10 +42,10 @@ struct Many {
   static constexpr int kTile = 128 * D * 2;  // bytes of a 128-row fp16 tile
   static constexpr int kKOff = 2 * kTile;    // behind the two Q tiles
   static constexpr int kVOff = kKOff + 2 * kTile;
-  static constexpr int kScaleOff = kVOff + 2 * kTile;              // float4 [slots][8]
-  static constexpr int kMulOff = kScaleOff + kScaleSlots * 8 * 16;  // float [256]
+  static constexpr int kPageOff = kVOff + 2 * kTile;             // float4 [slots][8]
+  static constexpr int kMulOff = kPageOff + kPageSlots * 8 * 16;  // float [256]
   static constexpr int kBarOff = kMulOff + 256 * 4;
-  static constexpr int kSmem = kBarOff + 256 + 1024;  // and room to align
+  static constexpr int kSmem = kBarOff + 512 + 1024;  // and room to align
   static constexpr uint32_t kIdescQK = (1u << 4) | (kKeys / 8 << 17) | (128 / 16 << 24);
   static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | (D / 8 << 17) | (128 / 16 << 24);
 };
@@ -55,14 +56,54 @@ enum {
   M_KEMPTY = 4,  // 2: its QKs done (commit)
   M_VFULL = 6,
   M_VEMPTY = 8,
-  M_SCALES = 10,  // 4: scales of a tile written (128)
-  M_SFULL = 14,   // 2: S in tensor memory (commit)
-  M_PHALF = 16,   // 2: P of keys 0..63 written (128)
-  M_PFULL = 18,   // 2: P written (128)
-  M_OFULL = 20,   // 2: last PV done (commit)
-  M_DONE = 22,    // 1: every MMA done (commit)
-  M_COUNT = 23
+  M_SFULL = 10,  // 2: S in tensor memory (commit)
+  M_PHALF = 12,  // 2: P of keys 0..63 written (128)
+  M_PFULL = 14,  // 2: P written (128)
+  M_OFULL = 16,  // 2: last PV done (commit)
+  M_DONE = 18,   // 1: every MMA done (commit)
+  M_PAGES = 19,  // 8: pages and scales of a tile written (32)
+  M_PFREE = 27,  // 8: every reader of them is done (one arrival)
+  M_COUNT = 35
 };
+
+// mbar_wait with a short loop: the clock is read once in 32 tries, so that
+// waiting warps leave the issue slots to the working ones.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
+  } while (global_timer_ns() - t0 < kWaitLimitNs);
+  atomicExch(err, (int)MMDIT_ETIMEOUT);
+  return false;
+}
+// The same by a whole warp that goes on together.
+__device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, err));
+}
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// s[i] = -inf for i >= lim.  Few tiles need it; group by group, so that the
+// compiler makes branches of it and not 128 selects that every tile runs.
+__device__ __forceinline__ void mask_row(float (&s)[kKeys], int lim) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    if (lim < 16 * g + 16) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (16 * g + i >= lim) s[16 * g + i] = -INFINITY;
+    }
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -79,10 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::kBarOff + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 8 * M_COUNT);
-  float4* scales = reinterpret_cast<float4*>(smem + C::kScaleOff);
+  float4* pages = reinterpret_cast<float4*>(smem + C::kPageOff);  // K scale, log2 and inverse of V's, id
   float* muls = reinterpret_cast<float*>(smem + C::kMulOff);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   int* err = A.err;
   const bool skip = *(volatile int*)err != 0;  // an earlier kernel timed out
 
@@ -98,7 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(M_PFULL + t), 128);
       mbar_init(bar(M_OFULL + t), 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) mbar_init(bar(M_SCALES + i), 128);
+    for (int i = 0; i < kPageSlots; ++i) {
+      mbar_init(bar(M_PAGES + i), 32);
+      mbar_init(bar(M_PFREE + i), 1);
+    }
     mbar_init(bar(M_DONE), 1);
     fence_mbar_init();
   }
@@ -109,64 +153,98 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp >= 12) {
     // ------------------------------------------------------------ MMA issuer
     // As P_t lies over S_t, tile t's order is QK(0), PV(0), QK(1), PV(1), ...;
     // the two row tiles alternate, so one's softmax runs under the other's MMAs.
+    // The whole warp runs the loop, so descriptors stay in uniform registers; one
+    // elected lane issues.
     setmaxnreg_dec<kRegsMma>();
-    if (warp == 12 && lane == 0 && !skip) {
+    if (warp == 12 && !skip) {
       bool ok = true;
       auto qk = [&](int t, int slot) {
         const uint64_t a = smem_desc_sw128(sbase + t * C::kTile, 16, 1024);
         const uint64_t b = smem_desc_sw128(sbase + C::kKOff + slot * C::kTile, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t at = (uint64_t)((k >> 2) * (kHalf >> 4) + (k & 3) * 2);
-          tc_mma_ss(tmem + t * 128, a + at, b + at, C::kIdescQK, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t at = (uint64_t)((k >> 2) * (kHalf >> 4) + (k & 3) * 2);
+            tc_mma_ss(tmem + t * 128, a + at, b + at, C::kIdescQK, k > 0);
+          }
+          tc_commit(bar(M_SFULL + t));
         }
-        tc_commit(bar(M_SFULL + t));
+        __syncwarp();
       };
       auto pv = [&](int t, int slot, int half, bool add) {
         const uint64_t b = smem_desc_sw128(sbase + C::kVOff + slot * C::kTile, kHalf, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_ts(tmem + 256 + t * D, tmem + t * 128 + (4 * half + k) * 8,
-                    b + (uint64_t)((4 * half + k) * 128), C::kIdescPV, add || half + k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc_mma_ts(tmem + 256 + t * D, tmem + t * 128 + (4 * half + k) * 8,
+                      b + (uint64_t)((4 * half + k) * 128), C::kIdescPV, add || half + k > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](int i) {
+        if (elect_one()) tc_commit(bar(i));
+        __syncwarp();
       };
       if (tiles > 0) {
-        for (int t = 0; t < nt && ok; ++t) ok = mbar_wait(bar(M_QREADY + t), 0, err);
-        ok = ok && mbar_wait(bar(M_KFULL), 0, err);
+        for (int t = 0; t < nt && ok; ++t) ok = wait_for(bar(M_QREADY + t), 0, err);
+        ok = __all_sync(0xffffffffu, ok && wait_for(bar(M_KFULL), 0, err));
         if (ok) {
           tc_fence_after();
           for (int t = 0; t < nt; ++t) qk(t, 0);
-          tc_commit(bar(M_KEMPTY));
+          commit(M_KEMPTY);
         }
         for (int j = 0; j < tiles && ok; ++j) {
           const int sv = j & 1, sk = sv ^ 1;
           const bool more = j + 1 < tiles;
-          if (!(ok = mbar_wait(bar(M_VFULL + sv), (j >> 1) & 1, err))) break;
+          if (!(ok = all_wait(bar(M_VFULL + sv), (j >> 1) & 1, err))) break;
           for (int t = 0; t < nt; ++t) {
-            if (!(ok = mbar_wait(bar(M_PHALF + t), j & 1, err))) break;
+            if (!(ok = all_wait(bar(M_PHALF + t), j & 1, err))) break;
             tc_fence_after();
             pv(t, sv, 0, j > 0);
-            if (!(ok = mbar_wait(bar(M_PFULL + t), j & 1, err))) break;
+            if (!(ok = all_wait(bar(M_PFULL + t), j & 1, err))) break;
             tc_fence_after();
             pv(t, sv, 1, true);
-            if (t == nt - 1) tc_commit(bar(M_VEMPTY + sv));
+            if (t == nt - 1) commit(M_VEMPTY + sv);
             if (more) {
-              if (t == 0 && !(ok = mbar_wait(bar(M_KFULL + sk), ((j + 1) >> 1) & 1, err))) break;
+              if (t == 0 && !(ok = all_wait(bar(M_KFULL + sk), ((j + 1) >> 1) & 1, err))) break;
               tc_fence_after();
               qk(t, sk);
-              if (t == nt - 1) tc_commit(bar(M_KEMPTY + sk));
+              if (t == nt - 1) commit(M_KEMPTY + sk);
             }
           }
+          // tile j is converted and both softmaxes have written their P
+          if (lane == 0) mbar_arrive(bar(M_PFREE + j % kPageSlots));
         }
       }
-      for (int t = 0; t < nt; ++t) tc_commit(bar(M_OFULL + t));
-      tc_commit(bar(M_DONE));
-      mbar_wait(bar(M_DONE), 0, err);
+      for (int t = 0; t < nt; ++t) commit(M_OFULL + t);
+      commit(M_DONE);
+      wait_for(bar(M_DONE), 0, err);
+    } else if (warp == 13 && !skip) {
+      // ---------------------------------------------------------- pages
+      // Lane g < 8 looks up group g of every tile.  A page that is not there is not
+      // seen; a V scale of 0 (held as inverse -1) stands for zeros.
+      bool ok = true;
+      for (int j = 0; j < tiles && ok; ++j) {
+        float4 x = make_float4(0.f, -INFINITY, 1.f, __int_as_float(-1));
+        const int n = w.lo + j * kKeys + (lane & 7) * 16;
+        const int page = n < w.hi ? page_of(A, w.b, n) : -1;
+        if (page >= 0) {
+          const long long at = (long long)page * A.Hk + w.hk;
+          const float vs = __ldg(A.v_scale + at);
+          x = make_float4(__ldg(A.k_scale + at), vs > 0.f ? log2f(vs) : 0.f,
+                          vs > 0.f ? 1.f / vs : -1.f, __int_as_float(page));
+        }
+        if (j >= kPageSlots)
+          ok = all_wait(bar(M_PFREE + j % kPageSlots), (j / kPageSlots - 1) & 1, err);
+        if (lane < 8) pages[(j % kPageSlots) * 8 + lane] = x;
+        if (ok) mbar_arrive(bar(M_PAGES + j % kPageSlots));
+      }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters
@@ -181,46 +259,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
     const int gpp = A.page >> 4;  // 16-token groups per page
     const int n0 = w.lo + cw * 32;
-    // pages of the warp's two groups in tile j; -1: nothing to load
-    auto find = [&](int j, int (&p)[2]) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int n = n0 + j * kKeys + f * 16;
-        p[f] = n < w.hi ? page_of(A, w.b, n) : -1;
-      }
+    int pg[2];  // pages of the warp's two groups; -1: nothing to load
+    bool ok = !skip;
+    // the pages of tile j; returns which of the groups have a V scale
+    auto find = [&](int j) {
+      const int slot = j % kPageSlots;
+      ok = all_wait(bar(M_PAGES + slot), (j / kPageSlots) & 1, err);
+      const float4 a = pages[slot * 8 + cw * 2], b = pages[slot * 8 + cw * 2 + 1];
+      pg[0] = ok ? __float_as_int(a.w) : -1;
+      pg[1] = ok ? __float_as_int(b.w) : -1;
+      return (a.z > 0.f ? 1 : 0) | (b.z > 0.f ? 2 : 0);
     };
-    // this half warp's scales
-    auto find_scales = [&](const int (&p)[2], float& k, float& v) {
-      const int page = lane < 16 ? p[0] : p[1];
-      k = v = 0.f;
-      if (page >= 0) {
-        k = __ldg(A.k_scale + (long long)page * A.Hk + w.hk);
-        v = __ldg(A.v_scale + (long long)page * A.Hk + w.hk);
-      }
-    };
-    // Writes them for the softmax and returns which groups have a V scale.  A page
-    // that is not there is not seen; a V scale of 0 stands for zeros.
-    auto put_scales = [&](int j, const int (&p)[2], float k, float v) {
-      const int page = lane < 16 ? p[0] : p[1];
-      if ((lane & 15) == 0)
-        scales[(j % kScaleSlots) * 8 + cw * 2 + (lane >> 4)] =
-            make_float4(k, page < 0 ? -INFINITY : (v > 0.f ? log2f(v) : 0.f),
-                        v > 0.f ? 1.f / v : 1.f, 0.f);
-      mbar_arrive(bar(M_SCALES + j % kScaleSlots));
-      return __ballot_sync(0xffffffffu, v > 0.f);
-    };
-    auto load = [&](const uint8_t* codes, int j, const int (&p)[2], uint4 (&r)[NI]) {
+    auto load = [&](const uint8_t* codes, int j, uint4 (&r)[NI]) {
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
         const int n = n0 + j * kKeys + f * 16;
         const uint8_t* src =
-            codes + (((long long)p[f] * A.Hk + w.hk) * gpp + ((n >> 4) & (gpp - 1))) * (16 * D) +
+            codes + (((long long)pg[f] * A.Hk + w.hk) * gpp + ((n >> 4) & (gpp - 1))) * (16 * D) +
             row * D + half * 64 + c4 * 16;
-        const int rows = p[f] >= 0 ? w.hi - n - row : 0;  // of this thread's tokens and later ones
+        uint4* to = r + f * (NI / 2);
+        if (pg[f] >= 0 && n + 16 <= w.hi) {  // the whole group is there
 #pragma unroll
-        for (int i = 0; i < NI / 2; ++i) {
-          r[f * (NI / 2) + i] = make_uint4(0u, 0u, 0u, 0u);
-          if (i * RS < rows) r[f * (NI / 2) + i] = __ldg(reinterpret_cast<const uint4*>(src + i * RS * D));
+          for (int i = 0; i < NI / 2; ++i)
+            to[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RS * D));
+        } else {
+          const int rows = pg[f] >= 0 ? w.hi - n - row : 0;  // of this thread's tokens and later ones
+#pragma unroll
+          for (int i = 0; i < NI / 2; ++i) {
+            to[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (i * RS < rows) to[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RS * D));
+          }
         }
       }
     };
@@ -239,45 +307,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     uint4 kr[NI], vr[NI];
-    int pg[2], pg2[2];  // pages of the next tile and of the one behind it
-    float sk, sv;
-    uint32_t scaled = 0;
-    bool ok = !skip;
-    if (tiles > 0) {
-      find(0, pg);
-      find(1, pg2);
-      find_scales(pg, sk, sv);
-      load(A.k, 0, pg, kr);
-      load(A.v, 0, pg, vr);
-      scaled = put_scales(0, pg, sk, sv);
+    int scaled = 0;  // groups of the V codes in flight that have a scale
+    if (tiles > 0 && ok) {
+      scaled = find(0);
+      load(A.k, 0, kr);
+      load(A.v, 0, vr);
     }
     for (int j = 0; j < tiles && ok; ++j) {
       const int slot = j & 1;
       const uint32_t free = ((j >> 1) & 1) ^ 1;
       const bool more = j + 1 < tiles;
-      pg[0] = pg2[0], pg[1] = pg2[1];
-      if (more) {
-        find_scales(pg, sk, sv);
-        find(j + 2, pg2);
-      }
-      if (!(ok = mbar_wait(bar(M_KEMPTY + slot), free, err))) break;
+      if (!(ok = wait_for(bar(M_KEMPTY + slot), free, err))) break;
       store(smem + C::kKOff + slot * C::kTile, kr);
       fence_proxy_async_smem();
       mbar_arrive(bar(M_KFULL + slot));
-      if (more) load(A.k, j + 1, pg, kr);
-      if (!(ok = mbar_wait(bar(M_VEMPTY + slot), free, err))) break;
+      int next = 0;
+      if (more) {
+        next = find(j + 1);
+        load(A.k, j + 1, kr);
+      }
+      if (!ok || !(ok = wait_for(bar(M_VEMPTY + slot), free, err))) break;
+      if (scaled != 3) {  // no scale: zeros
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (!(scaled >> (i >= NI / 2 ? 16 : 0) & 1u)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < NI; ++i)
+          if (!(scaled >> (i >= NI / 2) & 1)) vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
       store(smem + C::kVOff + slot * C::kTile, vr);
       fence_proxy_async_smem();
       mbar_arrive(bar(M_VFULL + slot));
-      if (more) {
-        load(A.v, j + 1, pg, vr);
-        // the slot's last readers, the softmaxes of tile j - 3, are behind the QK of
-        // tile j - 2, which was waited for above
-        scaled = put_scales(j + 1, pg, sk, sv);
-      }
+      if (more) load(A.v, j + 1, vr);
+      scaled = next;
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -330,9 +389,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;  // reference maximum of t, sum of weights
       bool ok = !skip;
       for (int j = 0; j < tiles; ++j) {
-        const int slot = j % kScaleSlots;
-        ok = ok && mbar_wait(bar(M_SCALES + slot), (j / kScaleSlots) & 1, err) &&
-             mbar_wait(bar(M_SFULL + t), j & 1, err);
+        const int slot = j % kPageSlots;
+        ok = ok && wait_for(bar(M_PAGES + slot), (j / kPageSlots) & 1, err) &&
+             wait_for(bar(M_SFULL + t), j & 1, err);
         if (__any_sync(0xffffffffu, !ok)) {
           ok = false;
           break;
@@ -356,18 +415,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int lim = min(limit, w.hi) - (w.lo + j * kKeys);
-        if (lim < kKeys) {
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i)
-            if (i >= lim) s[i] = -INFINITY;
-        }
+        if (__any_sync(0xffffffffu, lim < kKeys)) mask_row(s, lim);
         float mt = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const float* x = s + 16 * g;
           const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]), x[6]);
           const float b = max3f(max3f(x[7], x[8], x[9]), max3f(x[10], x[11], x[12]), x[13]);
-          const float4 sc = scales[slot * 8 + g];
+          const float4 sc = pages[slot * 8 + g];
           // at least the smallest normal number: -inf stays -inf
           const float f = fmaxf(mul * sc.x, 1.1754944e-38f);
           mt = fmaxf(mt, fmaf(max3f(a, b, fmaxf(x[14], x[15])), f, sc.y));
@@ -398,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int g = 2 * c; g < 2 * c + 2; ++g) {
-            const float4 sc = scales[slot * 8 + g];
+            const float4 sc = pages[slot * 8 + g];
             const float f = fmaxf(mul * sc.x, 1.1754944e-38f), d = sc.y + shift;
             const uint64_t f2 = pack_f32x2(f, f), d2 = pack_f32x2(d, d);
             uint64_t acc[2] = {0ull, 0ull};
@@ -414,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float a0, a1;
             unpack_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
-            l = fmaf(a0 + a1, sc.z, l);
+            l = fmaf(a0 + a1, fabsf(sc.z), l);
           }
           tmem_st16(s_addr + c * 16, pk);
           if (c == 1) {  // the first half of PV may start
@@ -429,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---------------------------------------------------------- epilogue
-      ok = ok && mbar_wait(bar(M_OFULL + t), 0, err);
+      ok = ok && wait_for(bar(M_OFULL + t), 0, err);
       if (__all_sync(0xffffffffu, ok)) {
         __syncwarp();
         tc_fence_after();
