@@ -34,7 +34,7 @@ constexpr int kPageSlots = 8;             // tiles whose pages and scales are he
 constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
 constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
 // registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
-constexpr int kRegsSoftmax = 176, kRegsConvert = 96, kRegsMma = 64;
+constexpr int kRegsSoftmax = 184, kRegsConvert = 96, kRegsMma = 48;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 512, "register split");
 
 template <int D>
@@ -105,7 +105,8 @@ __device__ __forceinline__ void mask_row(float (&s)[kKeys], int lim) {
   }
 }
 
-template <int D>
+// GP: 16-token groups per page.
+template <int D, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_many_kernel(const __grid_constant__ CacheAttnArgs A) {
   using C = Many<D>;
@@ -257,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cw = warp - 8;
     const int c4 = lane & 3, half = D == 128 ? (lane >> 3) & 1 : 0;
     const int row = ((lane >> 2) & 1) + 2 * (D == 128 ? lane >> 4 : lane >> 3);
-    const int gpp = A.page >> 4;  // 16-token groups per page
     const int n0 = w.lo + cw * 32;
     int pg[2];  // pages of the warp's two groups; -1: nothing to load
     bool ok = !skip;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int f = 0; f < 2; ++f) {
         const int n = n0 + j * kKeys + f * 16;
         const uint8_t* src =
-            codes + (((long long)pg[f] * A.Hk + w.hk) * gpp + ((n >> 4) & (gpp - 1))) * (16 * D) +
+            codes + (((long long)pg[f] * A.Hk + w.hk) * GP + ((n >> 4) & (GP - 1))) * (16 * D) +
             row * D + half * 64 + c4 * 16;
         uint4* to = r + f * (NI / 2);
         if (pg[f] >= 0 && n + 16 <= w.hi) {  // the whole group is there
@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       const float mul = muls[row];
-      const int limit = valid ? visible_keys(A, w.kv, w.ql, (w.r0 + row) / A.G) : 0;
+      // rows behind the last are computed with it and not stored
+      const int limit = visible_keys(A, w.kv, w.ql, (w.r0 + min(row, w.live - 1)) / A.G);
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_addr = tmem + lane_off + t * 128;
       const uint32_t o_addr = tmem + lane_off + 256 + t * D;
@@ -416,16 +417,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int lim = min(limit, w.hi) - (w.lo + j * kKeys);
         if (__any_sync(0xffffffffu, lim < kKeys)) mask_row(s, lim);
-        float mt = -INFINITY;
+        float f[8 / GP], y[8 / GP], mt = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
+          if (g % GP == 0) {
+            const float2 sc = *reinterpret_cast<const float2*>(pages + slot * 8 + g);
+            // at least the smallest normal number: -inf stays -inf
+            f[g / GP] = fmaxf(mul * sc.x, 1.1754944e-38f);
+            y[g / GP] = sc.y;
+          }
           const float* x = s + 16 * g;
           const float a = max3f(max3f(x[0], x[1], x[2]), max3f(x[3], x[4], x[5]), x[6]);
           const float b = max3f(max3f(x[7], x[8], x[9]), max3f(x[10], x[11], x[12]), x[13]);
-          const float4 sc = pages[slot * 8 + g];
-          // at least the smallest normal number: -inf stays -inf
-          const float f = fmaxf(mul * sc.x, 1.1754944e-38f);
-          mt = fmaxf(mt, fmaf(max3f(a, b, fmaxf(x[14], x[15])), f, sc.y));
+          mt = fmaxf(mt, fmaf(max3f(a, b, fmaxf(x[14], x[15])), f[g / GP], y[g / GP]));
         }
         const bool grow = mt > m + kGrow || (m == -INFINITY && mt > -INFINITY);
         if (__any_sync(0xffffffffu, grow)) {
@@ -448,15 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float shift = m == -INFINITY ? 0.f : kManyShift - m;
+        uint64_t acc[2] = {0ull, 0ull};  // sums of P of one page
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int g = 2 * c; g < 2 * c + 2; ++g) {
-            const float4 sc = pages[slot * 8 + g];
-            const float f = fmaxf(mul * sc.x, 1.1754944e-38f), d = sc.y + shift;
-            const uint64_t f2 = pack_f32x2(f, f), d2 = pack_f32x2(d, d);
-            uint64_t acc[2] = {0ull, 0ull};
+            const float d = y[g / GP] + shift;
+            const uint64_t f2 = pack_f32x2(f[g / GP], f[g / GP]), d2 = pack_f32x2(d, d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float p0, p1;
@@ -467,9 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[(g & 1) * 8 + i] = pack_half2(p0, p1);
               acc[i & 1] = add_f32x2(acc[i & 1], pack_f32x2(p0, p1));
             }
-            float a0, a1;
-            unpack_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
-            l = fmaf(a0 + a1, fabsf(sc.z), l);
+            if (g % GP == GP - 1) {
+              float a0, a1;
+              unpack_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
+              l = fmaf(a0 + a1, fabsf(pages[slot * 8 + g - (GP - 1)].z), l);
+              acc[0] = acc[1] = 0ull;
+            }
           }
           tmem_st16(s_addr + c * 16, pk);
           if (c == 1) {  // the first half of PV may start
@@ -557,24 +563,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, int GP>
 cudaError_t launch_many(const CacheAttnArgs& A, unsigned grid, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once_per_device(dev, [] {
-    return cudaFuncSetAttribute(cache_attn_many_kernel<D>,
+    return cudaFuncSetAttribute(cache_attn_many_kernel<D, GP>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Many<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  cache_attn_many_kernel<D><<<grid, kThreads, Many<D>::kSmem, s>>>(A);
+  cache_attn_many_kernel<D, GP><<<grid, kThreads, Many<D>::kSmem, s>>>(A);
   return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_many_pages(const CacheAttnArgs& A, unsigned grid, cudaStream_t s) {
+  switch (A.page) {
+    case 16: return launch_many<D, 1>(A, grid, s);
+    case 32: return launch_many<D, 2>(A, grid, s);
+    case 64: return launch_many<D, 4>(A, grid, s);
+    default: return launch_many<D, 8>(A, grid, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn_many(const CacheAttnArgs& A, int D, unsigned grid, cudaStream_t s) {
-  return D == 128 ? launch_many<128>(A, grid, s) : launch_many<64>(A, grid, s);
+  return D == 128 ? launch_many_pages<128>(A, grid, s) : launch_many_pages<64>(A, grid, s);
 }
 
 }  // namespace mmdit
