@@ -394,6 +394,31 @@ cudaError_t launch_append(AppendArgs& A, int batch, cudaStream_t s) {
   return launch_append_mode<T, 2>(A, grid, threads, smem, s);
 }
 
+// Every copy of a call runs at once: a page written twice, or read and written,
+// would end in either state.  One bit per page, kept by the thread and cleared
+// again: a list costs a few operations per entry, whatever the cache's size.
+int check_page_lists(int n, const int32_t* src, const int32_t* dst, int n_pages) {
+  thread_local std::vector<uint64_t> marks;
+  const size_t words = (size_t)n_pages / 64 + 1;
+  try {
+    if (marks.size() < words) marks.resize(words);
+  } catch (const std::bad_alloc&) {
+    return fail(MMDIT_EINVAL, "cache_copy_pages: no host memory for marks of %d pages", n_pages);
+  }
+  auto marked = [&](int page) { return (marks[page >> 6] >> (page & 63)) & 1u; };
+  int twice = -1, both = -1, seen = 0;
+  for (; seen < n && twice < 0; ++seen) {
+    if (marked(dst[seen])) twice = dst[seen];
+    marks[dst[seen] >> 6] |= 1ull << (dst[seen] & 63);
+  }
+  for (int i = 0; i < n && twice < 0 && both < 0; ++i)
+    if (marked(src[i])) both = src[i];
+  while (seen-- > 0) marks[dst[seen] >> 6] = 0;
+  if (twice >= 0) return fail(MMDIT_EINVAL, "cache_copy_pages: page %d is written twice", twice);
+  if (both >= 0) return fail(MMDIT_EINVAL, "cache_copy_pages: page %d is read and written", both);
+  return MMDIT_OK;
+}
+
 constexpr int kCopyPairs = 480;  // page pairs per launch: 3,840 bytes of parameters
 struct CopyArgs {
   uint8_t *k, *v;
@@ -489,23 +514,7 @@ int mmdit_cache_copy_pages(const mmdit_cache* cache, int n, const int32_t* src, 
     if (src[i] < 0 || src[i] >= cache->n_pages || dst[i] < 0 || dst[i] >= cache->n_pages)
       return fail(MMDIT_EINVAL, "cache_copy_pages: pair %d (%d -> %d) outside %d pages", i, src[i],
                   dst[i], cache->n_pages);
-  // every copy of the call runs at once: a page written twice, or read and
-  // written, would end in either state
-  try {
-    std::vector<int32_t> a(src, src + n), b(dst, dst + n);
-    std::sort(a.begin(), a.end());
-    std::sort(b.begin(), b.end());
-    if (std::adjacent_find(b.begin(), b.end()) != b.end())
-      return fail(MMDIT_EINVAL, "cache_copy_pages: page %d is written twice",
-                  *std::adjacent_find(b.begin(), b.end()));
-    for (size_t i = 0, j = 0; i < a.size() && j < b.size();) {
-      if (a[i] == b[j]) return fail(MMDIT_EINVAL, "cache_copy_pages: page %d is read and written", a[i]);
-      if (a[i] < b[j]) ++i;
-      else ++j;
-    }
-  } catch (const std::bad_alloc&) {
-    return fail(MMDIT_EINVAL, "cache_copy_pages: no host memory for a list of %d pages", n);
-  }
+  if ((rc = check_page_lists(n, src, dst, cache->n_pages))) return rc;
   if ((rc = check_sm100())) return rc;
   CopyArgs A;
   A.k = (uint8_t*)cache->k;

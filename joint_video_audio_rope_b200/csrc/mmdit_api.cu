@@ -173,13 +173,16 @@ int check_sm100() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 0)
-    return fail(MMDIT_EUNSUPPORTED, "device %d is sm_%d%d; this library targets sm_100a", dev,
-                major, minor);
-  return MMDIT_OK;
+  // a device's capability does not change: asked for once per device
+  e = once_per_device(dev, [dev] {
+    int major = 0, minor = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    return major == 10 && minor == 0 ? cudaSuccess : cudaErrorNoKernelImageForDevice;
+  });
+  if (e == cudaErrorNoKernelImageForDevice)
+    return fail(MMDIT_EUNSUPPORTED, "device %d is no sm_100; this library targets sm_100a", dev);
+  return e == cudaSuccess ? MMDIT_OK : cuda_fail(e, "device capability");
 }
 
 // Split of the video keys for the audio-query direction: enough splits that

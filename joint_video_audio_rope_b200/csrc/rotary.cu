@@ -226,8 +226,14 @@ int make_rotary_tab(const mmdit_rotary_params* r, int head_dim, RotaryTab& tab) 
     const double d = dims[a];
     double theta = r->theta;
     if (r->scaling == MMDIT_SCALE_NTK && dims[a] > 2) theta *= pow(f, d / (d - 2.0));
+    // theta^(-2i/d) from 8 fine and up to 8 coarse powers: one more rounding, 2^-53
+    double fine[8], coarse[8];
+    for (int i = 0; i < 8; ++i) {
+      fine[i] = pow(theta, -2.0 * i / d);
+      coarse[i] = 16 * i < dims[a] ? pow(theta, -16.0 * i / d) : 0.0;
+    }
     for (int i = 0; i < dims[a] / 2; ++i, ++m) {
-      double w = pow(theta, -2.0 * i / d);
+      double w = fine[i & 7] * coarse[i >> 3];
       if (r->scaling == MMDIT_SCALE_LINEAR) w /= f;
       if (r->scaling == MMDIT_SCALE_PARTS) {
         const double turns = r->trained[a] * w / (2.0 * pi);

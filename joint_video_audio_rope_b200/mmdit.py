@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
+from array import array
 from typing import Iterable, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -125,8 +126,7 @@ _SIGS = {
     "mmdit_cache_attn": (C.c_int, [_P, _P, _D, _D, _C, _P, _P, C.c_int, C.c_float, _P, _P,
                                    C.c_size_t, _P]),
     "mmdit_cache_attn_workspace_size": (C.c_size_t, [_D, _C]),
-    "mmdit_cache_copy_pages": (C.c_int, [_C, C.c_int, C.POINTER(C.c_int32), C.POINTER(C.c_int32),
-                                         _P]),
+    "mmdit_cache_copy_pages": (C.c_int, [_C, C.c_int, _P, _P, _P]),
     "mmdit_device_status": (C.c_int, [_P]),
     "mmdit_selftest_wait_timeout": (C.c_int, [C.c_int, _P, _P]),
     "mmdit_last_error": (C.c_char_p, []),
@@ -196,17 +196,25 @@ def rope_params(theta: float, dim_t: int, dim_h: int, dim_w: int) -> RopeParams:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device, without the Stream object that
+    torch.cuda.current_stream builds (2 us of a small call's 10)."""
+    global _current_stream
+    import torch
+    torch.cuda.init()
+    raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -428,9 +436,9 @@ def rotary(q, q_out, q_desc, q_out_desc, k, k_out, k_desc, k_out_desc, layout: L
            params: RotaryParams, first=None, transpose: bool = False, stream=None) -> None:
     """q_out = R q and k_out = R k (transpose: R^T, the gradient) at the positions of the
     layout's tokens first[b] + n; q or k may be None with its three companions."""
-    _check(_lib.mmdit_rotary(_ptr(q), _ptr(q_out), _ref(q_desc), _ref(q_out_desc), _ptr(k),
-                             _ptr(k_out), _ref(k_desc), _ref(k_out_desc), C.byref(layout),
-                             C.byref(params), _ptr(first), 1 if transpose else 0,
+    _check(_lib.mmdit_rotary(_ptr(q), _ptr(q_out), q_desc, q_out_desc, _ptr(k),
+                             _ptr(k_out), k_desc, k_out_desc, layout,
+                             params, _ptr(first), 1 if transpose else 0,
                              _stream(stream)))
 
 
@@ -459,12 +467,12 @@ def cache_append(k, v, desc: TensorDesc, cache: Cache, start, count=None,
                  stream=None) -> None:
     """Stores tokens start[b] .. start[b] + count[b] - 1 (int32 [B] on the device; count None:
     all N) in 8 bits; with layout and rotation, K is turned on the way."""
-    _check(_lib.mmdit_cache_append(_ptr(k), _ptr(v), C.byref(desc), C.byref(cache), _ptr(start),
-                                   _ptr(count), _ref(layout), _ref(rotation), _stream(stream)))
+    _check(_lib.mmdit_cache_append(_ptr(k), _ptr(v), desc, cache, _ptr(start),
+                                   _ptr(count), layout, rotation, _stream(stream)))
 
 
 def cache_attn_workspace_size(q_desc: TensorDesc, cache: Cache) -> int:
-    return _lib.mmdit_cache_attn_workspace_size(C.byref(q_desc), C.byref(cache))
+    return _lib.mmdit_cache_attn_workspace_size(q_desc, cache)
 
 
 def cache_attn(q, o, q_desc: TensorDesc, o_desc: TensorDesc, cache: Cache, kv_len, scale: float,
@@ -473,8 +481,8 @@ def cache_attn(q, o, q_desc: TensorDesc, o_desc: TensorDesc, cache: Cache, kv_le
     """o = softmax(q K^T * scale) V over the first kv_len[b] cached tokens (int32 [B] on the
     device); causal_block = c: a row sees its own and earlier blocks of c tokens.  Workspace from
     cache_attn_workspace_size."""
-    _check(_lib.mmdit_cache_attn(_ptr(q), _ptr(o), C.byref(q_desc), C.byref(o_desc),
-                                 C.byref(cache), _ptr(kv_len), _ptr(q_len), causal_block, scale,
+    _check(_lib.mmdit_cache_attn(_ptr(q), _ptr(o), q_desc, o_desc,
+                                 cache, _ptr(kv_len), _ptr(q_len), causal_block, scale,
                                  _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
@@ -483,8 +491,9 @@ def cache_copy_pages(cache: Cache, src: Sequence[int], dst: Sequence[int], strea
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst differ in length")
-    ids = C.c_int32 * max(n, 1)
-    _check(_lib.mmdit_cache_copy_pages(C.byref(cache), n, ids(*src), ids(*dst), _stream(stream)))
+    src, dst = array("i", src), array("i", dst)  # C int32, an eighth of a ctypes array's time
+    _check(_lib.mmdit_cache_copy_pages(cache, n, src.buffer_info()[0], dst.buffer_info()[0],
+                                       _stream(stream)))
 
 
 def num_blocks(layout: Layout) -> int:
