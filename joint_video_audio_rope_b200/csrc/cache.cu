@@ -1,13 +1,15 @@
 // The paged 8-bit K/V cache: storing new tokens (mmdit_cache_append) and
 // copying pages (mmdit_cache_copy_pages).  Attention over it: cache_attn.cu.
 //
-// Append.  One CTA takes one page of one item and a slice of the heads.  Per
-// head it holds the page's new rows of K and V in registers, finds max |x|
-// of both with one block reduction, and writes codes and scales: each value
-// is read once (2 or 4 bytes) and written once (1 byte), so the call is HBM
-// bound.  A scale is a power of two: e4m3 has its own exponent, so a finer scale would
-// buy no precision, and dividing by it, or moving a page to a larger one,
-// rounds nothing but the code itself.
+// Append.  One CTA takes one page of one item and a slice of the heads, and
+// finds the page's angles once, into shared memory.  Per head it holds the new rows
+// of K and V in registers (NV 16-byte vectors of each per thread, so that a few
+// CTAs per SM keep enough loads in flight), finds max |x| of both with one
+// block reduction, and writes codes and scales: each value is read once (2 or
+// 4 bytes) and written once (1 byte), so the call is HBM bound.  A scale is a
+// power of two: e4m3 has its own exponent, so a finer scale would buy no precision,
+// and dividing by it, or moving a page to a larger one, rounds nothing but the code
+// itself.
 //
 // Copy.  The page lists travel in the kernel's parameters: no list has to be
 // copied to the device first, and one launch moves up to kCopyPairs pages.
@@ -79,7 +81,7 @@ namespace {
 struct AppendArgs {
   const void *k, *v;
   long long st, sb;
-  int N, slice, mode;  // mode: 0 K as it is, 1 interleaved pairs, 2 half pairs
+  int N, slice, cluster, mode;  // mode: 0 K as it is, 1 interleaved pairs, 2 half pairs
   const int32_t *start, *count;
   mmdit_cache c;
   int* err;
@@ -132,47 +134,85 @@ __device__ __forceinline__ void values_of(const uint4& r, float (&x)[4], float*)
   for (int i = 0; i < 4; ++i) x[i] = p[i];
 }
 
-// Maximum over the block; `red` is read until the next call with the other buffer.
-__device__ __forceinline__ float block_max(float x, float* red, int tid, int warps) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  if ((tid & 31) == 0) red[tid >> 5] = x;
-  __syncthreads();
-  x = red[tid & 31 & (warps - 1)];  // a power of two of warps
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-  return x;
+// Maxima that a NaN wins.  Non-negative values order as their bits do, infinity and
+// NaN above every number, so the rest of a reduction runs on integers.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
-
-// The new scale of one half of a (page, head) that holds `older` rows already,
-// whose codes move to it if it has grown.
-__device__ __forceinline__ float settle_scale(float amax, float* scale, uint8_t* codes, int older,
-                                              int D, int tid, int threads) {
-  float s = fit_scale(amax);
-  if (older > 0) {
-    const float old = *scale;
-    s = fmaxf(s, floor_scale(old));
-    if (s > old) {
-      const float f = old / s;
-      uint32_t* w = reinterpret_cast<uint32_t*>(codes);
-      for (int i = tid; i < older * D / 4; i += threads) {
-        const float2 a = value2(w[i] & 0xffffu), c = value2(w[i] >> 16);
-        w[i] = codes4(a.x * f, a.y * f, c.x * f, c.y * f);
-      }
-    }
-    __syncthreads();  // every thread has read the old scale
+__device__ __forceinline__ uint32_t abs_bits(float a, float b, uint32_t m) {
+  return __float_as_uint(max3_nan(fabsf(a), fabsf(b), __uint_as_float(m)));
+}
+// bits of the largest |x| of a raw vector and of `m`
+__device__ __forceinline__ uint32_t vector_max(const uint4& r, uint32_t m, __nv_bfloat16*) {
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t p =
+      __vmaxu2(__vmaxu2(r.x & k, r.y & k), __vmaxu2(r.z & k, r.w & k));
+  return max(m, max(p & 0xffff0000u, p << 16));
+}
+__device__ __forceinline__ uint32_t vector_max(const uint4& r, uint32_t m, float*) {
+  m = abs_bits(__uint_as_float(r.x), __uint_as_float(r.y), m);
+  return abs_bits(__uint_as_float(r.z), __uint_as_float(r.w), m);
+}
+// Zeros in place of infinities and NaN; false if there were any.
+__device__ __forceinline__ bool keep_numbers(uint4& r, __nv_bfloat16*) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u, ok = false;
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu, ok = false;
   }
-  if (tid == 0) *scale = s;
-  return s;
+  return ok;
+}
+__device__ __forceinline__ bool keep_numbers(uint4& r, float*) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0u, ok = false;
+  return ok;
 }
 
-// 16 values of K and of V per thread: page * D / 16 threads.
-template <typename T, int MODE>
-__global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ AppendArgs A) {
-  constexpr int E = 16 / sizeof(T), NV = 16 / E, P = E / 2;
-  extern __shared__ __align__(16) uint8_t smem[];  // half pairs: raw K rows, then their codes
-  __shared__ float red[2][32];
-  __shared__ uint32_t bad[2][4];  // rows with an infinity or NaN in K or V
+// Moves the codes of a page's older rows to a scale that has grown.
+__device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float f, int tid,
+                                              int threads) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+  for (int i = tid; i < n / 4; i += threads) {
+    const float2 a = value2(w[i] & 0xffffu), c = value2(w[i] >> 16);
+    w[i] = codes4(a.x * f, a.y * f, c.x * f, c.y * f);
+  }
+}
+
+constexpr int kAppendCluster = 8;  // most CTAs that share a page's angles
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// x at the shared address `to` of the cluster's CTA `rank`
+__device__ __forceinline__ void store_cluster(uint32_t to, int rank, float2 x) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(to),
+      "r"(rank), "f"(x.x), "f"(x.y)
+      : "memory");
+}
+
+// MODE: 0 K as it is, 1 interleaved pairs, 2 half pairs.  page * D / (NV 16-byte
+// vectors) threads.
+// MAXT: most threads; three CTAs of 256 per SM (up to 80 registers), or two with
+// eight vectors, keep 96 to 128 KB in flight.
+template <typename T, int MODE, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) append_kernel(const __grid_constant__ AppendArgs A) {
+  constexpr int E = 16 / sizeof(T), P = E / 2;
+  // angles [page][D / 2] (cos, sin), then for half pairs: K rows in 32 bits
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint2 red[2][16];  // by head parity: maxima of V and K per warp
+  __shared__ uint32_t lost[4];  // rows with an infinity or NaN in K or V
+  __shared__ double place[MODE == 0 ? 1 : 128][3];  // positions of the page's new rows
   const mmdit_cache& C = A.c;
   const int page = C.page_tokens, D = C.head_dim;
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5;
@@ -193,205 +233,255 @@ __global__ void __launch_bounds__(1024) append_kernel(const __grid_constant__ Ap
 
   const int cpr = D / E;  // vectors per row
   const int chunk = tid % cpr, row0 = tid / cpr, rstep = threads / cpr;
-  // angles: interleaved, P pairs of each of NV rows; half, one pair of 8 rows
-  constexpr int NA = MODE == 1 ? NV * P : (MODE == 2 ? 8 : 1);
-  float cs[NA], sn[NA];
+  float2* angles = reinterpret_cast<float2*>(smem);
+  float* tile = reinterpret_cast<float*>(smem + (size_t)page * D * 4);
   const int m2 = tid % (D / 2), prow0 = tid / (D / 2), pstep = threads / (D / 2);
   int ch1 = 0, ch2 = 0;
-  if constexpr (MODE == 1) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      double pt, ph, pw;
-      token_position_f64(A.layout, p * page + row0 + i * rstep, pt, ph, pw);
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const int m = chunk * P + j;
-        if (m < A.tab.np) rotary_cos_sin(A.tab, m, pt, ph, pw, cs[i * P + j], sn[i * P + j]);
+  if constexpr (MODE == 2) rotary_channels(A.tab, m2, ch1, ch2);
+  if constexpr (MODE != 0) {
+    // The CTAs of a cluster share the page: each finds its part of the angles and
+    // writes it to all of them.
+    cluster_arrive();
+    if (tid < r_hi - r_lo) {
+      double* at = place[r_lo + tid];
+      token_position_f64(A.layout, p * page + r_lo + tid, at[0], at[1], at[2]);
+    }
+    __syncthreads();
+    const int size = A.cluster, rank = blockIdx.y % size;
+    cluster_wait();  // every CTA of the cluster has started
+    for (int row = r_lo + rank * pstep + prow0; row < r_hi; row += size * pstep) {
+      float2 cs = make_float2(1.f, 0.f);
+      if (m2 < A.tab.np) {
+        const double* at = place[row];
+        rotary_cos_sin(A.tab, m2, at[0], at[1], at[2], cs.x, cs.y);
       }
+      const uint32_t to = smem_u32(angles + row * (D / 2) + m2);
+      for (int r = 0; r < size; ++r) store_cluster(to, r, cs);
     }
+    cluster_arrive();
+    cluster_wait();
   }
-  if constexpr (MODE == 2) {
-    rotary_channels(A.tab, m2, ch1, ch2);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      double pt, ph, pw;
-      token_position_f64(A.layout, p * page + prow0 + i * pstep, pt, ph, pw);
-      if (m2 < A.tab.np) rotary_cos_sin(A.tab, m2, pt, ph, pw, cs[i], sn[i]);
-    }
-  }
-  if (tid < 8) bad[tid >> 2][tid & 3] = 0u;
-  __syncthreads();
 
+  constexpr uint32_t kInf = 0x7f800000u;
   const int h0 = blockIdx.y * A.slice, h1 = min(C.heads, h0 + A.slice);
   for (int h = h0; h < h1; ++h) {
-    uint32_t* lost = bad[(h - h0) & 1];
+    const int par = (h - h0) & 1;
+    const long long from = b * A.sb + tok0 * A.st + (long long)h * D + chunk * E;
     uint4 kr[NV], vr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int row = row0 + i * rstep;
       kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
       if (row >= r_lo && row < r_hi) {
-        const long long at = b * A.sb + (tok0 + row) * A.st + (long long)h * D + chunk * E;
-        vr[i] = *reinterpret_cast<const uint4*>((const T*)A.v + at);
-        kr[i] = *reinterpret_cast<const uint4*>((const T*)A.k + at);
+        kr[i] = __ldcs(reinterpret_cast<const uint4*>((const T*)A.k + from + row * A.st));
+        vr[i] = __ldcs(reinterpret_cast<const uint4*>((const T*)A.v + from + row * A.st));
       }
     }
     const long long ph = (long long)id * C.heads + h;
     uint8_t* kc = (uint8_t*)C.k + ph * page * D;
     uint8_t* vc = (uint8_t*)C.v + ph * page * D;
-    float x[E];
+    float old_k = 0.f, old_v = 0.f;
+    if (r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
 
-    // ---- V: what is not a number becomes 0, and its row is marked
-    float am = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      values_of(vr[i], x, (T*)nullptr);
-      bool ok = true;
-#pragma unroll
-      for (int j = 0; j < E; ++j) {
-        if (is_number(x[j])) am = fmaxf(am, fabsf(x[j]));
-        else ok = false;
-      }
-      if (!ok) {
-        const int row = row0 + i * rstep;
-        atomicOr(&lost[row >> 5], 1u << (row & 31));
-      }
-      if constexpr (MODE == 2)
-        *reinterpret_cast<uint4*>(smem + (size_t)(tid + i * threads) * 16) = kr[i];
-    }
-    am = block_max(am, red[0], tid, warps);
-    // the next head's marks: the last ones there were read before that barrier
-    if (tid < 4) bad[(h - h0 + 1) & 1][tid] = 0u;
-    float s = settle_scale(am, C.v_scale + ph, vc, r_lo, D, tid, threads);
-    float is = inverse_pow2(s);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int row = row0 + i * rstep;
-      if (row < r_lo || row >= r_hi) continue;
-      values_of(vr[i], x, (T*)nullptr);
-      uint32_t w[E / 4];
-#pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = is_number(x[j]) ? x[j] * is : 0.f;
-#pragma unroll
-      for (int j = 0; j < E / 4; ++j)
-        w[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(vc + row * D + chunk * E) = make_uint2(w[0], w[1]);
-      else
-        *reinterpret_cast<uint32_t*>(vc + row * D + chunk * E) = w[0];
-    }
-
-    // ---- K, turned
-    float kx[16];
-    am = 0.f;
+    // ---- K turned: interleaved pairs in kx, half pairs in the tile; the largest |x|
+    float kx[MODE == 1 ? NV * E : 1];
+    uint32_t mv = 0u, mk = 0u;
     if constexpr (MODE == 2) {
-      // the raw rows were complete at block_max's barrier
-      const T* raw = reinterpret_cast<const T*>(smem);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = prow0 + i * pstep;
-        const float x1 = (float)raw[row * D + ch1], x2 = (float)raw[row * D + ch2];
-        if (!is_number(x1) || !is_number(x2)) atomicOr(&lost[row >> 5], 1u << (row & 31));
-        const bool turned = m2 < A.tab.np;
-        kx[2 * i] = turned ? x1 * cs[i] - x2 * sn[i] : x1;
-        kx[2 * i + 1] = turned ? x1 * sn[i] + x2 * cs[i] : x2;
-      }
-    } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
+        float x[E];
         values_of(kr[i], x, (T*)nullptr);
-        bool ok = true;
+        float4* to = reinterpret_cast<float4*>(tile + (row0 + i * rstep) * D + chunk * E);
 #pragma unroll
-        for (int j = 0; j < E; ++j) ok = ok && is_number(x[j]);
-        if (!ok) {
-          const int row = row0 + i * rstep;
-          atomicOr(&lost[row >> 5], 1u << (row & 31));
-        }
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          float x1 = x[2 * j], x2 = x[2 * j + 1];
-          if (MODE == 1 && chunk * P + j < A.tab.np) {
-            x1 = x[2 * j] * cs[(i * P + j) % NA] - x[2 * j + 1] * sn[(i * P + j) % NA];
-            x2 = x[2 * j] * sn[(i * P + j) % NA] + x[2 * j + 1] * cs[(i * P + j) % NA];
-          }
-          kx[i * E + 2 * j] = x1;
-          kx[i * E + 2 * j + 1] = x2;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (is_number(kx[j])) am = fmaxf(am, fabsf(kx[j]));
-    am = block_max(am, red[1], tid, warps);
-    s = settle_scale(am, C.k_scale + ph, kc, r_lo, D, tid, threads);
-    is = inverse_pow2(s);
-    if constexpr (MODE == 2) {
-      uint8_t* tile = smem + (size_t)page * D * sizeof(T);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = prow0 + i * pstep;
-        const uint32_t two = codes4(kx[2 * i] * is, kx[2 * i + 1] * is, 0.f, 0.f);
-        tile[row * D + ch1] = (uint8_t)two;
-        tile[row * D + ch2] = (uint8_t)(two >> 8);
+        for (int j = 0; j < E / 4; ++j)
+          to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
       }
       __syncthreads();
+#pragma unroll 4
+      for (int row = r_lo + prow0; row < r_hi; row += pstep) {
+        float &y1 = tile[row * D + ch1], &y2 = tile[row * D + ch2];
+        const float x1 = y1, x2 = y2;
+        const float2 cs = angles[row * (D / 2) + m2];
+        const float t1 = x1 * cs.x - x2 * cs.y, t2 = x1 * cs.y + x2 * cs.x;
+        y1 = t1;
+        y2 = t2;
+        mk = abs_bits(t1, t2, mk);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      mv = vector_max(vr[i], mv, (T*)nullptr);
+      if constexpr (MODE == 0) mk = vector_max(kr[i], mk, (T*)nullptr);
+      if constexpr (MODE == 1) {
+        float x[E];
+        values_of(kr[i], x, (T*)nullptr);
+        const int row = row0 + i * rstep;
+        // rows without a new token hold zeros; their angles are not there
+        const float2* a = angles + min(max(row, r_lo), r_hi - 1) * (D / 2) + chunk * P;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float2 cs = a[j];
+          const float t1 = x[2 * j] * cs.x - x[2 * j + 1] * cs.y;
+          const float t2 = x[2 * j] * cs.y + x[2 * j + 1] * cs.x;
+          kx[i * E + 2 * j] = t1;
+          kx[i * E + 2 * j + 1] = t2;
+          mk = abs_bits(t1, t2, mk);
+        }
+      }
+    }
+    auto turned = [&](int i, float (&x)[E]) {  // vector i of K
+      if constexpr (MODE == 0) values_of(kr[i], x, (T*)nullptr);
+      if constexpr (MODE == 1) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] = kx[i * E + j];
+      }
+      if constexpr (MODE == 2) {
+        const float4* t = reinterpret_cast<const float4*>(tile + (row0 + i * rstep) * D + chunk * E);
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j)
+          x[4 * j] = t[j].x, x[4 * j + 1] = t[j].y, x[4 * j + 2] = t[j].z, x[4 * j + 3] = t[j].w;
+      }
+    };
+    auto block_max = [&](uint2* r) {
+      mv = __reduce_max_sync(0xffffffffu, mv);
+      mk = __reduce_max_sync(0xffffffffu, mk);
+      if ((tid & 31) == 0) r[tid >> 5] = make_uint2(mv, mk);
+      __syncthreads();
+      for (int i = 0; i < warps; ++i) {
+        const uint2 m = r[i];
+        mv = max(mv, m.x);
+        mk = max(mk, m.y);
+      }
+    };
+    block_max(red[par]);
+    const bool careful = max(mv, mk) >= kInf;  // the same in every thread
+    if (careful) {
+      // an infinity or NaN: mark its rows, leave it out of V and of the maxima
+      __syncthreads();
+      if (tid < 4) lost[tid] = 0u;
+      __syncthreads();
+      mv = mk = 0u;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * rstep;
+        if (row < r_lo || row >= r_hi) continue;
+        bool ok = keep_numbers(vr[i], (T*)nullptr);
+        mv = vector_max(vr[i], mv, (T*)nullptr);
+        uint4 raw = *reinterpret_cast<const uint4*>((const T*)A.k + from + row * A.st);
+        ok = keep_numbers(raw, (T*)nullptr) && ok;
+        if (!ok) atomicOr(&lost[row >> 5], 1u << (row & 31));
+        float x[E];
+        turned(i, x);
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+          if (is_number(x[j])) mk = abs_bits(x[j], 0.f, mk);
+      }
+      block_max(red[par]);
+    }
+
+    // ---- scales; every thread has read the old ones before that barrier
+    float sv = fit_scale(__uint_as_float(mv)), sk = fit_scale(__uint_as_float(mk));
+    if (r_lo > 0) {
+      sv = fmaxf(sv, floor_scale(old_v));
+      sk = fmaxf(sk, floor_scale(old_k));
+      if (sv > old_v) rescale_codes(vc, r_lo * D, old_v / sv, tid, threads);
+      if (sk > old_k) rescale_codes(kc, r_lo * D, old_k / sk, tid, threads);
+    }
+    if (tid == 0) {
+      C.v_scale[ph] = sv;
+      C.k_scale[ph] = sk;
+    }
+    const float iv = inverse_pow2(sv), ik = inverse_pow2(sk);
+
+    // ---- codes
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int row = row0 + i * rstep;
       if (row < r_lo || row >= r_hi) continue;
-      uint32_t w[E / 4];
+      const int to = row * D + chunk * E;
+      uint32_t w[E / 4], v[E / 4];
+      float x[E];
+      values_of(vr[i], x, (T*)nullptr);
 #pragma unroll
-      for (int j = 0; j < E / 4; ++j) {
-        if constexpr (MODE == 2)
-          w[j] = *reinterpret_cast<const uint32_t*>(smem + (size_t)page * D * sizeof(T) + row * D +
-                                                    chunk * E + 4 * j);
-        else
-          w[j] = codes4(kx[i * E + 4 * j] * is, kx[i * E + 4 * j + 1] * is,
-                        kx[i * E + 4 * j + 2] * is, kx[i * E + 4 * j + 3] * is);
-        if ((lost[row >> 5] >> (row & 31)) & 1u) w[j] = 0x7f7f7f7fu;
+      for (int j = 0; j < E / 4; ++j)
+        v[j] = codes4(x[4 * j] * iv, x[4 * j + 1] * iv, x[4 * j + 2] * iv, x[4 * j + 3] * iv);
+      turned(i, x);
+#pragma unroll
+      for (int j = 0; j < E / 4; ++j)
+        w[j] = codes4(x[4 * j] * ik, x[4 * j + 1] * ik, x[4 * j + 2] * ik, x[4 * j + 3] * ik);
+      if (careful && ((lost[row >> 5] >> (row & 31)) & 1u)) {
+#pragma unroll
+        for (int j = 0; j < E / 4; ++j) w[j] = 0x7f7f7f7fu;
       }
-      if constexpr (E == 8)
-        *reinterpret_cast<uint2*>(kc + row * D + chunk * E) = make_uint2(w[0], w[1]);
-      else
-        *reinterpret_cast<uint32_t*>(kc + row * D + chunk * E) = w[0];
+      if constexpr (E == 8) {
+        *reinterpret_cast<uint2*>(vc + to) = make_uint2(v[0], v[1]);
+        *reinterpret_cast<uint2*>(kc + to) = make_uint2(w[0], w[1]);
+      } else {
+        *reinterpret_cast<uint32_t*>(vc + to) = v[0];
+        *reinterpret_cast<uint32_t*>(kc + to) = w[0];
+      }
     }
   }
 }
 
-template <typename T, int MODE>
-cudaError_t launch_append_mode(const AppendArgs& A, dim3 grid, int threads, size_t smem,
-                               cudaStream_t s) {
-  if (MODE == 2) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    e = once_per_device(dev, [] {
-      return cudaFuncSetAttribute(append_kernel<T, MODE>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  128 * 128 * ((int)sizeof(T) + 1));
-    });
-    if (e != cudaSuccess) return e;
+template <typename T, int MODE, int NV, int MAXT>
+cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
+  const int page = A.c.page_tokens, D = A.c.head_dim;
+  const int threads = page * D * (int)sizeof(T) / (16 * NV);
+  const int smem = page * D * 4 * MODE;  // angles, K rows
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once_per_device(dev, [] {
+    return cudaFuncSetAttribute(append_kernel<T, MODE, NV, MAXT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                128 * 128 * 4 * MODE);
+  });
+  if (e != cudaSuccess) return e;
+  const int pages = (A.N + page - 2) / page + 1;  // most pages that N tokens touch
+  // Heads per CTA: the look-ups of a page are done once for all of them, so as many
+  // as leave three full waves of CTAs (about 1,024 threads per SM).  Where K is turned, the
+  // CTAs of a page form clusters of up to eight that share the work on its angles (480p
+  // clip, bf16: 200 us when each of four CTAs finds them all).
+  const long long ctas = (long long)pages * batch * A.c.heads;
+  const long long wave = 148LL * (1024 / threads);
+  A.slice = (int)std::max(1LL, std::min<long long>(A.c.heads, ctas / (3 * wave)));
+  int slices = (A.c.heads + A.slice - 1) / A.slice, size = 1;
+  if (MODE != 0) {
+    while (size < kAppendCluster && 2 * size <= slices) size *= 2;
+    slices = (slices + size - 1) / size * size;
   }
-  append_kernel<T, MODE><<<grid, threads, MODE == 2 ? smem : 0, s>>>(A);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pages, slices, batch);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.y = size;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  A.cluster = size;
+  return cudaLaunchKernelEx(&cfg, append_kernel<T, MODE, NV, MAXT>, A);
+}
+
+template <typename T, int NV, int MAXT>
+cudaError_t launch_append_pairs(AppendArgs& A, int batch, cudaStream_t s) {
+  if (A.mode == 0) return launch_append_mode<T, 0, NV, MAXT>(A, batch, s);
+  if (A.mode == 1) return launch_append_mode<T, 1, NV, MAXT>(A, batch, s);
+  return launch_append_mode<T, 2, NV, MAXT>(A, batch, s);
 }
 
 template <typename T>
 cudaError_t launch_append(AppendArgs& A, int batch, cudaStream_t s) {
-  const int page = A.c.page_tokens, D = A.c.head_dim;
-  const int threads = page * D / 16;
-  const int pages = (A.N + page - 2) / page + 1;  // most pages that N tokens touch
-  // Heads per CTA: the angles of a page are found once for all of them, so as
-  // many as leave two full waves of CTAs.
-  const long long ctas = (long long)pages * batch * A.c.heads;
-  const long long wave = 148LL * (1024 / threads);
-  A.slice = (int)std::max(1LL, std::min<long long>(A.c.heads, ctas / (2 * wave)));
-  const dim3 grid(pages, (A.c.heads + A.slice - 1) / A.slice, batch);
-  const size_t smem = (size_t)page * D * (sizeof(T) + 1);
-  if (A.mode == 0) return launch_append_mode<T, 0>(A, grid, threads, 0, s);
-  if (A.mode == 1) return launch_append_mode<T, 1>(A, grid, threads, 0, s);
-  return launch_append_mode<T, 2>(A, grid, threads, smem, s);
+  // 4 vectors per thread, 8 where that would take more than 256 threads (one CTA of
+  // 512 fills an SM less than two of 256 with twice the loads each)
+  const int vectors = A.c.page_tokens * A.c.head_dim * (int)sizeof(T) / 16;
+  if (vectors <= 1024) return launch_append_pairs<T, 4, 256>(A, batch, s);
+  if constexpr (sizeof(T) == 4)
+    if (vectors > 2048) return launch_append_pairs<T, 8, 512>(A, batch, s);
+  return launch_append_pairs<T, 8, 256>(A, batch, s);
 }
 
 // Every copy of a call runs at once: a page written twice, or read and written,
