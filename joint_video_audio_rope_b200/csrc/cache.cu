@@ -236,8 +236,20 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
   float2* angles = reinterpret_cast<float2*>(smem);
   float* tile = reinterpret_cast<float*>(smem + (size_t)page * D * 4);
   const int m2 = tid % (D / 2), prow0 = tid / (D / 2), pstep = threads / (D / 2);
+  // Interleaved bf16 pairs: a thread reads four angles as two 16-byte vectors.  The first
+  // vectors of a row's chunks come first, then the second ones, so that
+  // neighbouring threads read neighbouring vectors (no bank conflicts).
+  const int angle_at =
+      MODE == 1 && P == 4 ? (m2 & 1) | (m2 >> 2) << 1 | ((m2 >> 1) & 1) * (D / 4) : m2;
+  // Half pairs: vectors of four channels of K; every second group of eight vectors swaps
+  // its neighbours, for the same reason.
+  auto swap = [](int ch) { return ch ^ ((ch >> 3) & 4); };
   int ch1 = 0, ch2 = 0;
-  if constexpr (MODE == 2) rotary_channels(A.tab, m2, ch1, ch2);
+  if constexpr (MODE == 2) {
+    rotary_channels(A.tab, m2, ch1, ch2);
+    ch1 = swap(ch1);
+    ch2 = swap(ch2);
+  }
   if constexpr (MODE != 0) {
     // The CTAs of a cluster share the page: each finds its part of the angles and
     // writes it to all of them.
@@ -255,7 +267,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
         const double* at = place[row];
         rotary_cos_sin(A.tab, m2, at[0], at[1], at[2], cs.x, cs.y);
       }
-      const uint32_t to = smem_u32(angles + row * (D / 2) + m2);
+      const uint32_t to = smem_u32(angles + row * (D / 2) + angle_at);
       for (int r = 0; r < size; ++r) store_cluster(to, r, cs);
     }
     cluster_arrive();
@@ -291,21 +303,35 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
       for (int i = 0; i < NV; ++i) {
         float x[E];
         values_of(kr[i], x, (T*)nullptr);
-        float4* to = reinterpret_cast<float4*>(tile + (row0 + i * rstep) * D + chunk * E);
+        float* to = tile + (row0 + i * rstep) * D;
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j)
-          to[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        for (int j = 0; j < E; j += 4)
+          *reinterpret_cast<float4*>(to + swap(chunk * E + j)) =
+              make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
       }
       __syncthreads();
-#pragma unroll 4
-      for (int row = r_lo + prow0; row < r_hi; row += pstep) {
-        float &y1 = tile[row * D + ch1], &y2 = tile[row * D + ch2];
-        const float x1 = y1, x2 = y2;
-        const float2 cs = angles[row * (D / 2) + m2];
-        const float t1 = x1 * cs.x - x2 * cs.y, t2 = x1 * cs.y + x2 * cs.x;
-        y1 = t1;
-        y2 = t2;
-        mk = abs_bits(t1, t2, mk);
+      // four rows at a time: all loads, then all stores, which the compiler may not
+      // move past one another
+      for (int row = r_lo + prow0; row < r_hi; row += 4 * pstep) {
+        float x1[4], x2[4];
+        float2 cs[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = min(row + u * pstep, r_hi - 1);
+          x1[u] = tile[r * D + ch1];
+          x2[u] = tile[r * D + ch2];
+          cs[u] = angles[r * (D / 2) + m2];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = row + u * pstep;
+          if (r >= r_hi) break;
+          const float t1 = x1[u] * cs[u].x - x2[u] * cs[u].y;
+          const float t2 = x1[u] * cs[u].y + x2[u] * cs[u].x;
+          tile[r * D + ch1] = t1;
+          tile[r * D + ch2] = t2;
+          mk = abs_bits(t1, t2, mk);
+        }
       }
     }
 #pragma unroll
@@ -317,10 +343,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
         values_of(kr[i], x, (T*)nullptr);
         const int row = row0 + i * rstep;
         // rows without a new token hold zeros; their angles are not there
-        const float2* a = angles + min(max(row, r_lo), r_hi - 1) * (D / 2) + chunk * P;
+        const float4* a = reinterpret_cast<const float4*>(
+            angles + min(max(row, r_lo), r_hi - 1) * (D / 2)) + chunk;
+        float4 two;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
-          const float2 cs = a[j];
+          if (j % 2 == 0) two = a[j / 2 * (D / 8)];
+          const float2 cs = j % 2 ? make_float2(two.z, two.w) : make_float2(two.x, two.y);
           const float t1 = x[2 * j] * cs.x - x[2 * j + 1] * cs.y;
           const float t2 = x[2 * j] * cs.y + x[2 * j + 1] * cs.x;
           kx[i * E + 2 * j] = t1;
@@ -336,10 +365,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
         for (int j = 0; j < E; ++j) x[j] = kx[i * E + j];
       }
       if constexpr (MODE == 2) {
-        const float4* t = reinterpret_cast<const float4*>(tile + (row0 + i * rstep) * D + chunk * E);
+        const float* t = tile + (row0 + i * rstep) * D;
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j)
-          x[4 * j] = t[j].x, x[4 * j + 1] = t[j].y, x[4 * j + 2] = t[j].z, x[4 * j + 3] = t[j].w;
+        for (int j = 0; j < E; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(t + swap(chunk * E + j));
+          x[j] = f.x, x[j + 1] = f.y, x[j + 2] = f.z, x[j + 3] = f.w;
+        }
       }
     };
     auto block_max = [&](uint2* r) {
@@ -439,14 +470,21 @@ cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const int pages = (A.N + page - 2) / page + 1;  // most pages that N tokens touch
-  // Heads per CTA: the look-ups of a page are done once for all of them, so as many
-  // as leave three full waves of CTAs (about 1,024 threads per SM).  Where K is turned, the
-  // CTAs of a page form clusters of up to eight that share the work on its angles (480p
-  // clip, bf16: 200 us when each of four CTAs finds them all).
-  const long long ctas = (long long)pages * batch * A.c.heads;
-  const long long wave = 148LL * (1024 / threads);
-  A.slice = (int)std::max(1LL, std::min<long long>(A.c.heads, ctas / (3 * wave)));
-  int slices = (A.c.heads + A.slice - 1) / A.slice, size = 1;
+  // Slices of the heads, one CTA each: a CTA takes as long as its heads and about two
+  // more for the page's look-ups and angles, and about 768 threads fit an SM; the number of
+  // slices with the shortest waves is taken (480p clip, bf16, interleaved: 136 us with 4
+  // slices, 157 with 2, 160 with 12).  Where K is turned, the CTAs of a page form clusters of
+  // up to eight that share the work on its angles (the same with clusters of 1: 200 us).
+  const long long resident = 148LL * std::max(1, 768 / threads);
+  int slices = 1, size = 1;
+  long long best = 0;
+  for (int n = 1; n <= std::min(A.c.heads, 256); n += n < 8 ? n : 8) {
+    const long long waves = ((long long)pages * batch * n + resident - 1) / resident;
+    const long long cost = waves * ((A.c.heads + n - 1) / n + 2);
+    if (n == 1 || cost < best) best = cost, slices = n;
+  }
+  A.slice = (A.c.heads + slices - 1) / slices;
+  slices = (A.c.heads + A.slice - 1) / A.slice;
   if (MODE != 0) {
     while (size < kAppendCluster && 2 * size <= slices) size *= 2;
     slices = (slices + size - 1) / size * size;
