@@ -2,22 +2,23 @@
 // merge of split key ranges.
 //
 // Few rows (single tokens, a frame's audio tokens; every fp32 call).  The codes
-// are read once and barely used, so the call is bound by HBM: the kernel
-// keeps K and V in registers on their way from memory to the tensor cores.  A
-// warp owns slabs of S tokens; a thread's 16-byte loads of codes are turned into
-// fp16 pairs that are mma.m16n8k16 operands as they stand, because the order of
-// channels inside a contraction (K) and of output channels (V) is free:
+// are read once and barely used, so the call is bound by HBM: what counts is
+// bytes in flight.  A warp owns slabs of 32 tokens and copies the codes of the next ones into
+// its own ring in shared memory (cp.async, no barrier between warps) while it computes
+// the current one.  16-byte vectors of codes are turned into fp16 pairs that are
+// mma.m16n8k16 operands as they stand, because the order of channels inside a contraction (K) and of
+// output channels (V) is free:
 //   scores  A = Q (16 rows x 16 channels), B = K^T: thread (g, t) of a warp (g =
 //           lane / 4, t = lane % 4) holds channels 16 t .. 16 t + 15 of token g;
 //           step kk contracts channels 16 t + 4 kk .. + 3 of every t
 //   output  A = P (the score fragment as it is), B = V: thread (g, t) holds
 //           channels g D/8 .. of tokens 2t, 2t + 1, 2t + 8, 2t + 9; output tile j
 //           holds channel g D/8 + j of every g
+// The vectors of a slab's rows are permuted so that both reads meet every bank once.
 // e4m3 is exact in fp16.  Q is multiplied by a power of two per row that puts
 // its largest value at 2^14..2^15, so bf16 values are exact in fp16 too down
 // to 2^-29 of that; fp32 values are split into two fp16 parts (22 bits), and so
-// are the probabilities of an fp32 call.  The next slab's loads are in flight
-// while the current one is computed.  Each warp runs its own softmax; the CTA's
+// are the probabilities of an fp32 call.  Each warp runs its own softmax; the CTA's
 // warps, then the key ranges, are merged at the end in a fixed order.
 #include <math.h>
 
@@ -61,25 +62,113 @@ __device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
   }
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Shared memory of a warp's ring: per stage the slab's codes of K and V and, per
+// 16 tokens, their scales and whether their page is there.
+template <typename T, int D>
+struct Few {
+  static constexpr bool kF32 = sizeof(T) == 4;
+  static constexpr int S = kF32 ? 16 : 32;  // tokens per slab
+  static constexpr int kStages = kF32 ? 4 : 3;
+  static constexpr int kCodes = S * D;
+  static constexpr int kStage = 2 * kCodes + 32;
+  static constexpr int kRing = kFewWarps * kStages * kStage;
+  static constexpr int kMerge = kFewWarps * 16 * ((D + 4) + 2) * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+};
+
+// Offset of 16-byte vector c of row r of a slab, permuted within 128 bytes: rows g,
+// g + 1 (K, vectors t) and rows 2t (V, vectors g, g + 1) each cover all eight
+// positions.
+template <int D>
+__device__ __forceinline__ int slab_at(int r, int c) {
+  if constexpr (D == 128) return r * 128 + ((c ^ (r & 6) ^ ((r & 1) << 2)) << 4);
+  else return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ (r & 6)) << 4);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kFewWarps * 32, 2)
     cache_attn_few_kernel(const __grid_constant__ CacheAttnArgs A) {
-  constexpr bool kF32 = sizeof(T) == 4;
-  constexpr int S = kF32 ? 16 : 32;   // tokens per slab
+  using F = Few<T, D>;
+  constexpr bool kF32 = F::kF32;
+  constexpr int S = F::S;             // tokens per slab
+  constexpr int ST = F::kStages;
   constexpr int KK = D / 16;          // contraction steps over the channels
   constexpr int KV = D / 64;          // 16-byte code vectors per thread and token of K
   constexpr int NT = D / 8;           // output tiles
   constexpr int VW = D / 32;          // words of codes per thread and token of V
   constexpr int QP = kF32 ? 2 : 1;    // fp16 parts of Q and P
-  __shared__ float sm_o[kFewWarps][16][D + 4];
-  __shared__ float sm_ml[kFewWarps][16][2];
+  extern __shared__ __align__(128) uint8_t smem[];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be launched
   const CacheItem w = item_of(A, blockIdx.x, kFewTile);
   const int b = w.b, hk = w.hk, r0 = w.r0, kv = w.kv, ql = w.ql, live = w.live;
   const int lo = w.lo, hi = w.hi;
   if (live <= 0) return;
+
+  // ---- the ring: copies of the slab at token n into a stage
+  constexpr int HF = S / 16;  // 16-token halves of a slab: one page each at most
+  uint8_t* ring = smem + warp * (ST * F::kStage);
+  auto find = [&](int n, int (&id)[HF]) {
+#pragma unroll
+    for (int f = 0; f < HF; ++f) id[f] = n + 16 * f < hi ? page_of(A, b, n + 16 * f) : -1;
+  };
+  auto copy = [&](int n, const int (&id)[HF], int stage) {
+    uint8_t* to = ring + stage * F::kStage;
+    const uint32_t dst = smem_u32(to);
+#pragma unroll
+    for (int f = 0; f < HF; ++f) {
+      const long long page = (long long)max(id[f], 0) * A.Hk + hk;
+      const long long from = (page * A.page + ((n + 16 * f) & (A.page - 1))) * D + lane * 16;
+      // the group's 16 D bytes are consecutive
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int v = lane + 32 * i, row = v / (D / 16), c = v % (D / 16);
+        const bool there = id[f] >= 0 && n + 16 * f + row < hi;
+        const long long at = there ? from + i * 512 : 0;
+        cp_async16(dst + slab_at<D>(16 * f + row, c), A.k + at, there);
+        cp_async16(dst + F::kCodes + slab_at<D>(16 * f + row, c), A.v + at, there);
+      }
+      if (lane == f) {
+        float* m = reinterpret_cast<float*>(to + 2 * F::kCodes) + 4 * f;
+        m[2] = id[f] < 0 ? -INFINITY : 0.f;
+        if (id[f] >= 0) {
+          cp_async4(smem_u32(m), A.k_scale + page);
+          cp_async4(smem_u32(m + 1), A.v_scale + page);
+        } else {
+          m[0] = m[1] = 0.f;
+        }
+      }
+    }
+  };
+  constexpr int kStep = kFewWarps * S;
+  const int n0 = lo + warp * S;
+  int next[HF];  // pages of the slab that is copied next
+  find(n0, next);
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) {
+    const int n = n0 + i * kStep;
+    if (n < hi) copy(n, next, i);
+    cp_async_commit();
+    find(n + kStep, next);
+  }
 
   // ---- Q fragments of rows g and g + 8, and the rows' visible keys
   uint32_t qa[QP][KK][4];
@@ -124,92 +213,45 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  constexpr int HF = S / 16;  // 16-token halves of a slab: one page each at most
-  const long long head_bytes = (long long)A.page * D;
-  auto find = [&](int n, int (&id)[HF]) {
-#pragma unroll
-    for (int f = 0; f < HF; ++f) id[f] = n + 16 * f < hi ? page_of(A, b, n + 16 * f) : -1;
-  };
-  uint4 kr[S / 8][KV];
-  uint32_t vr[S / 16][4][VW];
-  float ks[HF], vs[HF];
-  auto load_k = [&](int n, const int (&id)[HF]) {
-#pragma unroll
-    for (int nt = 0; nt < S / 8; ++nt) {
-      const int tok = n + nt * 8 + g, pg = id[nt >> 1];
-      const uint8_t* p = A.k + ((long long)pg * A.Hk + hk) * head_bytes + (tok & (A.page - 1)) * D;
-#pragma unroll
-      for (int c = 0; c < KV; ++c)
-        kr[nt][c] = (pg >= 0 && tok < hi)
-                        ? __ldg(reinterpret_cast<const uint4*>(p + c * 64 + t * 16))
-                        : make_uint4(0u, 0u, 0u, 0u);
+  int stage = 0;
+  for (int n = n0; n < hi; n += kStep) {
+    cp_async_wait<ST - 2>();
+    __syncwarp();
+    {  // the stage read last is free: the copies of the slab ST - 1 ahead
+      const int ahead = n + (ST - 1) * kStep;
+      if (ahead < hi) copy(ahead, next, stage == 0 ? ST - 1 : stage - 1);
+      cp_async_commit();
+      find(ahead + kStep, next);
     }
-#pragma unroll
-    for (int f = 0; f < HF; ++f)
-      ks[f] = id[f] >= 0 ? __ldg(A.k_scale + (long long)id[f] * A.Hk + hk) : 0.f;
-  };
-  auto load_v = [&](int n, const int (&id)[HF]) {
-#pragma unroll
-    for (int f = 0; f < HF; ++f) {
-      vs[f] = id[f] >= 0 ? __ldg(A.v_scale + (long long)id[f] * A.Hk + hk) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = n + f * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-        const uint8_t* p = A.v + ((long long)id[f] * A.Hk + hk) * head_bytes +
-                           (tok & (A.page - 1)) * D + g * (D / 8);
-        const bool in = id[f] >= 0 && tok < hi;
-        if constexpr (D == 128) {
-          const uint4 w = in ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-          vr[f][i][0] = w.x, vr[f][i][1] = w.y, vr[f][i][2] = w.z, vr[f][i][3] = w.w;
-        } else {
-          const uint2 w = in ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0u, 0u);
-          vr[f][i][0] = w.x, vr[f][i][1] = w.y;
-        }
-      }
-    }
-  };
-
-  int n = lo + warp * S, id[HF], id2[HF];
-  if (n < hi) {
-    find(n, id);
-    load_k(n, id);
-    load_v(n, id);
-    find(n + kFewWarps * S, id2);
-  }
-  for (; n < hi; n += kFewWarps * S) {
-    const int n2 = n + kFewWarps * S;
+    const uint8_t* kc = ring + stage * F::kStage;
+    const uint8_t* vc = kc + F::kCodes;
+    const float4* meta = reinterpret_cast<const float4*>(vc + F::kCodes);
+    stage = stage == ST - 1 ? 0 : stage + 1;
     // ---- scores
     float sc[S / 8][4];
 #pragma unroll
     for (int nt = 0; nt < S / 8; ++nt) {
       sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        const uint4& r = kr[nt][kk >> 2];
-        const uint32_t w = (kk & 3) == 0 ? r.x : (kk & 3) == 1 ? r.y : (kk & 3) == 2 ? r.z : r.w;
-        const uint32_t b0 = half2_of(w & 0xffffu), b1 = half2_of(w >> 16);
+      for (int c = 0; c < KV; ++c) {
+        const uint4 r = *reinterpret_cast<const uint4*>(kc + slab_at<D>(nt * 8 + g, c * 4 + t));
 #pragma unroll
-        for (int p = QP - 1; p >= 0; --p) mma16816(sc[nt], qa[p][kk], b0, b1);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w;
+          const uint32_t b0 = half2_of(x & 0xffffu), b1 = half2_of(x >> 16);
+#pragma unroll
+          for (int p = QP - 1; p >= 0; --p) mma16816(sc[nt], qa[p][c * 4 + k], b0, b1);
+        }
       }
     }
     float kf[HF], lv[HF], iv[HF];
 #pragma unroll
     for (int f = 0; f < HF; ++f) {
-      kf[f] = ks[f];
+      const float4 m4 = meta[f];
+      kf[f] = m4.x;
       // a page that is not there is not seen; a V scale of 0 stands for zeros
-      lv[f] = id[f] < 0 ? -INFINITY : (vs[f] > 0.f ? log2f(vs[f]) : 0.f);
-      iv[f] = vs[f] > 0.f ? 1.f / vs[f] : 1.f;
-      if (!(vs[f] > 0.f)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vr[f][i][w] = 0u;
-      }
-    }
-    int id3[HF];
-    if (n2 < hi) {
-      load_k(n2, id2);
-      find(n2 + kFewWarps * S, id3);
+      lv[f] = m4.z + (m4.y > 0.f ? log2f(m4.y) : 0.f);
+      iv[f] = m4.y > 0.f ? 1.f / m4.y : 0.f;
     }
     // ---- softmax of rows g (i = 0) and g + 8 (i = 1)
     bool grew = false;
@@ -254,7 +296,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         const int i = q & 1, nt = 2 * f + (q >> 1);
         float p0 = ex2_approx(sc[nt][2 * i] - mref[i]);
         float p1 = ex2_approx(sc[nt][2 * i + 1] - mref[i]);
-        l[i] = fmaf(p0 + p1, iv[f], l[i]);
+        l[i] = fmaf(p0 + p1, iv[f] > 0.f ? iv[f] : 1.f, l[i]);
 #pragma unroll
         for (int p = 0; p < QP; ++p) {
           const uint32_t h = pack_half2(p0, p1);
@@ -264,13 +306,30 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
           p1 -= y.y;
         }
       }
+      uint32_t vr[4][VW];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = f * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vc + slab_at<D>(row, g));
+          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][2] = x.z, vr[i][3] = x.w;
+        } else {
+          const uint2 x =
+              *reinterpret_cast<const uint2*>(vc + slab_at<D>(row, g >> 1) + (g & 1) * 8);
+          vr[i][0] = x.x, vr[i][1] = x.y;
+        }
+        if (!(iv[f] > 0.f)) {
+#pragma unroll
+          for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < NT; j += 4) {
         // four channels of tokens (2t, 2t + 1) and (2t + 8, 2t + 9), as pairs
-        const uint32_t a0 = __byte_perm(vr[f][0][j >> 2], vr[f][1][j >> 2], 0x5140);
-        const uint32_t a1 = __byte_perm(vr[f][0][j >> 2], vr[f][1][j >> 2], 0x7362);
-        const uint32_t c0 = __byte_perm(vr[f][2][j >> 2], vr[f][3][j >> 2], 0x5140);
-        const uint32_t c1 = __byte_perm(vr[f][2][j >> 2], vr[f][3][j >> 2], 0x7362);
+        const uint32_t a0 = __byte_perm(vr[0][j >> 2], vr[1][j >> 2], 0x5140);
+        const uint32_t a1 = __byte_perm(vr[0][j >> 2], vr[1][j >> 2], 0x7362);
+        const uint32_t c0 = __byte_perm(vr[2][j >> 2], vr[3][j >> 2], 0x5140);
+        const uint32_t c1 = __byte_perm(vr[2][j >> 2], vr[3][j >> 2], 0x7362);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t x = e < 2 ? a0 : a1, y = e < 2 ? c0 : c1;
@@ -289,15 +348,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         }
       }
     }
-    if (n2 < hi) load_v(n2, id2);
-#pragma unroll
-    for (int f = 0; f < HF; ++f) {
-      id[f] = id2[f];
-      id2[f] = n2 < hi ? id3[f] : -1;
-    }
   }
 
-  // ---- the CTA's warps, merged in their order
+  // ---- the CTA's warps, merged in their order; the rings are done with
+  cp_async_wait<0>();
+  __syncthreads();
+  float(*sm_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(smem);
+  float(*sm_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(smem + kFewWarps * 16 * (D + 4) * 4);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -369,34 +426,37 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
         L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
 }
 
-// Merges the key ranges of the split items in their order: a warp per row, a
-// lane for D / 32 channels.
-template <typename T, int D>
+// Merges the key ranges of the split items in a fixed order: WPR warps per row (warp
+// w takes ranges w, w + WPR, ..), a lane for D / 32 channels.  Launched while the
+// attention kernel still runs (its launch costs no time of its own) and waits for it here.
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(256)
     cache_attn_merge_kernel(const __grid_constant__ CacheAttnArgs A, int tile) {
   constexpr int W = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);  // over the split items' rows
+  __shared__ float part[WPR == 1 ? 1 : WPR][D + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = blockIdx.x * (8 / WPR) + warp / WPR;  // over the split items' rows
   const int item = i / tile, row = i % tile;
   int b, hk, r0;
   item_rows(A, A.whole + item, tile, b, hk, r0);
-  if (b >= A.B) return;
   const int r = r0 + row, tok = r / A.G, head = hk * A.G + r % A.G;
-  if (tok >= query_tokens(A, b)) return;
-  const long long step = tile;
+  const bool live = b < A.B && tok < query_tokens(A, b);  // the same in all warps of a row
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;
   const long long p0 = (long long)item * A.splits * tile + row;
   float M = -INFINITY;
-  for (int s = lane; s < A.splits; s += 32) M = fmaxf(M, A.part_ml[2 * (p0 + s * step)]);
+  for (int s = lane; s < A.splits; s += 32)
+    M = fmaxf(M, A.part_ml[2 * (p0 + (long long)s * tile)]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   const float Mr = M == -INFINITY ? 0.f : M;
   float L = 0.f, out[W] = {};
-#pragma unroll 4
-  for (int s = 0; s < A.splits; ++s) {
-    const long long pr = p0 + s * step;
+#pragma unroll 8
+  for (int s = warp % WPR; s < A.splits; s += WPR) {
+    const long long pr = p0 + (long long)s * tile;
     const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * pr);
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // an empty range
-    const float f = ex2_approx(ml.x - Mr);
+    // an empty range's sums are zeros: it adds nothing
+    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - Mr);
     L = fmaf(f, ml.y, L);
     const float* src = A.part_o + pr * D + lane * W;
 #pragma unroll
@@ -404,6 +464,22 @@ __global__ void __launch_bounds__(256)
       const float2 x = *reinterpret_cast<const float2*>(src + c);
       out[c] = fmaf(f, x.x, out[c]);
       out[c + 1] = fmaf(f, x.y, out[c + 1]);
+    }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int c = 0; c < W; ++c) part[warp][lane * W + c] = out[c];
+    if (lane == 0) part[warp][D] = L;
+    __syncthreads();
+    if (warp > 0) return;
+    L = 0.f;
+#pragma unroll
+    for (int c = 0; c < W; ++c) out[c] = 0.f;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      L += part[x][D];
+#pragma unroll
+      for (int c = 0; c < W; ++c) out[c] += part[x][lane * W + c];
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -467,14 +543,32 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
 
 template <typename T, int D>
 cudaError_t launch_few(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
-  cache_attn_few_kernel<T, D><<<(unsigned)p.grid(), kFewWarps * 32, 0, s>>>(A);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once_per_device(dev, [] {
+    return cudaFuncSetAttribute(cache_attn_few_kernel<T, D>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Few<T, D>::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  cache_attn_few_kernel<T, D><<<(unsigned)p.grid(), kFewWarps * 32, Few<T, D>::kSmem, s>>>(A);
   return cudaGetLastError();
 }
 template <typename T, int D>
 cudaError_t launch_merge(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
   const long long rows = (p.items - p.whole) * p.tile;
-  cache_attn_merge_kernel<T, D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(A, p.tile);
-  return cudaGetLastError();
+  const bool few = p.splits <= 8;  // a warp reads that many ranges at once
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(few ? (rows + 7) / 8 : rows));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, cache_attn_merge_kernel<T, D, 1>, A, p.tile)
+             : cudaLaunchKernelEx(&cfg, cache_attn_merge_kernel<T, D, 8>, A, p.tile);
 }
 template <typename T, int D>
 cudaError_t launch_cache_attn(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {

@@ -110,6 +110,7 @@ template <int D, int GP>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_many_kernel(const __grid_constant__ CacheAttnArgs A) {
   using C = Many<D>;
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be launched
   const CacheItem w = item_of(A, blockIdx.x, kManyTile);
   if (w.live <= 0) return;
   const int tiles = (w.hi - w.lo + kKeys - 1) / kKeys;  // 0: nothing to see
