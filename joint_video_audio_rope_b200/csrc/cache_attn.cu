@@ -7,13 +7,15 @@
 // its own ring in shared memory (cp.async, no barrier between warps) while it computes
 // the current one.  16-byte vectors of codes are turned into fp16 pairs that are
 // mma.m16n8k16 operands as they stand, because the order of channels inside a contraction (K) and of
-// output channels (V) is free:
-//   scores  A = Q (16 rows x 16 channels), B = K^T: thread (g, t) of a warp (g =
-//           lane / 4, t = lane % 4) holds channels 16 t .. 16 t + 15 of token g;
-//           step kk contracts channels 16 t + 4 kk .. + 3 of every t
-//   output  A = P (the score fragment as it is), B = V: thread (g, t) holds
-//           channels g D/8 .. of tokens 2t, 2t + 1, 2t + 8, 2t + 9; output tile j
-//           holds channel g D/8 + j of every g
+// output channels (V) is free.  Scores and outputs are formed transposed, so that a tile of up to
+// 8 query rows is one tile of 8 columns:
+//   S^T  A = K (16 tokens x 16 channels), B = Q^T: thread (g, t) of a warp (g = lane
+//        / 4, t = lane % 4) holds channels 16 t .. 16 t + 15 of tokens g and g + 8; step
+//        kk contracts channels 16 t + 4 kk .. + 3 of every t
+//   O^T  A = V^T (16 channels x 16 tokens), B = P^T: thread (g, t) holds channels
+//        g D/8 .. of tokens 2t, 2t + 1, 2t + 8, 2t + 9; output tile j holds channels
+//        g D/8 + 2j and + 2j + 1 of every g.  P^T is the score fragment with its
+//        8 x 8 blocks transposed (movmatrix).
 // The vectors of a slab's rows are permuted so that both reads meet every bank once.
 // e4m3 is exact in fp16.  Q is multiplied by a power of two per row that puts
 // its largest value at 2^14..2^15, so bf16 values are exact in fp16 too down
@@ -32,7 +34,7 @@ namespace {
 
 constexpr int kFewWarps = 4;
 // bf16 rows per (item, K/V head) up to which 16-row tiles are taken
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 16;
 // The largest probability of a row is held as 2^14: fp16 keeps its relative
 // precision down to 2^-14, so what is 2^-28 of the largest is still whole.
 constexpr float kShift = 14.f;
@@ -80,16 +82,19 @@ __device__ __forceinline__ void cp_async_wait() {
 
 // Shared memory of a warp's ring: per stage the slab's codes of K and V and, per
 // 16 tokens, their scales and whether their page is there.
-template <typename T, int D>
+template <typename T, int D, int NQ>
 struct Few {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int S = kF32 ? 16 : 32;  // tokens per slab
-  static constexpr int kStages = kF32 ? 4 : 3;
+  static constexpr int kCtas = D * NQ * (kF32 ? 2 : 1) >= 256 ? 2 : 3;  // per SM, by registers
   static constexpr int kCodes = S * D;
   static constexpr int kStage = 2 * kCodes + 32;
+  static constexpr int kFit = 222 * 1024 / (kCtas * kFewWarps * kStage);
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
   static constexpr int kRing = kFewWarps * kStages * kStage;
-  static constexpr int kMerge = kFewWarps * 16 * ((D + 4) + 2) * 4;
+  static constexpr int kMerge = kFewWarps * 8 * NQ * ((D + 4) + 2) * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static_assert(kStages >= 2, "a slab is copied while another is computed");
 };
 
 // Offset of 16-byte vector c of row r of a slab, permuted within 128 bytes: rows g,
@@ -101,35 +106,47 @@ __device__ __forceinline__ int slab_at(int r, int c) {
   else return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ (r & 6)) << 4);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kFewWarps * 32, 2)
+// 8 x 8 block of 16-bit values held as a fragment (row g, columns 2t, 2t + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// NQ: tiles of 8 query rows.
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
     cache_attn_few_kernel(const __grid_constant__ CacheAttnArgs A) {
-  using F = Few<T, D>;
+  using F = Few<T, D, NQ>;
   constexpr bool kF32 = F::kF32;
   constexpr int S = F::S;             // tokens per slab
   constexpr int ST = F::kStages;
+  constexpr int HF = S / 16;          // 16-token parts of a slab: one page each
   constexpr int KK = D / 16;          // contraction steps over the channels
   constexpr int KV = D / 64;          // 16-byte code vectors per thread and token of K
-  constexpr int NT = D / 8;           // output tiles
+  constexpr int NT = D / 16;          // output tiles
   constexpr int VW = D / 32;          // words of codes per thread and token of V
   constexpr int QP = kF32 ? 2 : 1;    // fp16 parts of Q and P
+  constexpr int kTile = 8 * NQ;
   extern __shared__ __align__(128) uint8_t smem[];
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be launched
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;");  // the merge may be launched
-  const CacheItem w = item_of(A, blockIdx.x, kFewTile);
+  const CacheItem w = item_of(A, blockIdx.x, kTile);
   const int b = w.b, hk = w.hk, r0 = w.r0, kv = w.kv, ql = w.ql, live = w.live;
   const int lo = w.lo, hi = w.hi;
   if (live <= 0) return;
 
   // ---- the ring: copies of the slab at token n into a stage
-  constexpr int HF = S / 16;  // 16-token halves of a slab: one page each at most
   uint8_t* ring = smem + warp * (ST * F::kStage);
   auto find = [&](int n, int (&id)[HF]) {
 #pragma unroll
     for (int f = 0; f < HF; ++f) id[f] = n + 16 * f < hi ? page_of(A, b, n + 16 * f) : -1;
   };
+  // This thread's vectors of a group of 16 tokens: lane + 32 i.  Their places differ
+  // by 512 i, and for D = 128 by the permutation's bit of row 4.
+  const uint32_t place = slab_at<D>(lane / (D / 16), lane % (D / 16));
   auto copy = [&](int n, const int (&id)[HF], int stage) {
     uint8_t* to = ring + stage * F::kStage;
     const uint32_t dst = smem_u32(to);
@@ -137,14 +154,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     for (int f = 0; f < HF; ++f) {
       const long long page = (long long)max(id[f], 0) * A.Hk + hk;
       const long long from = (page * A.page + ((n + 16 * f) & (A.page - 1))) * D + lane * 16;
-      // the group's 16 D bytes are consecutive
+      const uint8_t *kp = A.k + from, *vp = A.v + from;  // 16 D consecutive bytes
+      const int rows = id[f] >= 0 ? hi - n - 16 * f : 0;
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
-        const int v = lane + 32 * i, row = v / (D / 16), c = v % (D / 16);
-        const bool there = id[f] >= 0 && n + 16 * f + row < hi;
-        const long long at = there ? from + i * 512 : 0;
-        cp_async16(dst + slab_at<D>(16 * f + row, c), A.k + at, there);
-        cp_async16(dst + F::kCodes + slab_at<D>(16 * f + row, c), A.v + at, there);
+        const uint32_t at =
+            dst + f * 16 * D + i * 512 + (D == 128 && (i & 1) ? place ^ 64u : place);
+        const bool there = (lane + 32 * i) / (D / 16) < rows;
+        cp_async16(at, there ? kp + i * 512 : A.k, there);
+        cp_async16(at + F::kCodes, there ? vp + i * 512 : A.v, there);
       }
       if (lane == f) {
         float* m = reinterpret_cast<float*>(to + 2 * F::kCodes) + 4 * f;
@@ -170,28 +188,26 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     find(n + kStep, next);
   }
 
-  // ---- Q fragments of rows g and g + 8, and the rows' visible keys
-  uint32_t qa[QP][KK][4];
-  float mul[2];
-  int limit[2];
+  // ---- Q fragments of rows 8 q + g; factors and visible keys of rows 8 q + 2t + e
+  uint32_t qb[QP][NQ][KK][2];
+  float mul[NQ][2];
+  int limit[NQ][2], full = hi;  // keys below `full` are seen by every row
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = r0 + g + 8 * i, tok = r / A.G, head = hk * A.G + r % A.G;
-    const bool row = g + 8 * i < live;
-    limit[i] = row ? visible_keys(A, kv, ql, tok) : 0;
-    const T* src = (const T*)A.q + b * A.q_sb + (long long)tok * A.q_st + (long long)head * D;
+  for (int q = 0; q < NQ; ++q) {
+    const int rr = 8 * q + g, r = r0 + rr;
+    const T* src = (const T*)A.q + b * A.q_sb + (long long)(r / A.G) * A.q_st +
+                   (long long)(hk * A.G + r % A.G) * D;
     float x[KK][4], am = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       x[kk][0] = x[kk][1] = x[kk][2] = x[kk][3] = 0.f;
-      if (row) load4(src + (kk >> 2) * 64 + t * 16 + (kk & 3) * 4, x[kk]);
+      if (rr < live) load4(src + (kk >> 2) * 64 + t * 16 + (kk & 3) * 4, x[kk]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) am = fmaxf(am, fabsf(x[kk][j]));
     }
     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
     const float f = fit_half(am);
-    mul[i] = A.scale_log2 / f;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
@@ -200,18 +216,34 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
 #pragma unroll
         for (int p = 0; p < QP; ++p) {
           const uint32_t h = pack_half2(x0, x1);
-          qa[p][kk][i + 2 * j] = h;
+          qb[p][q][kk][j] = h;
           const float2 y = unpack_half2(h);
           x0 -= y.x;
           x1 -= y.y;
         }
       }
-  }
-
-  float acc[NT][4];
+    const float m = A.scale_log2 / f;
 #pragma unroll
-  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int e = 0; e < 2; ++e) {
+      mul[q][e] = __shfl_sync(0xffffffffu, m, (2 * t + e) * 4);
+      // rows behind the last are computed with it and not stored
+      const int row = min(8 * q + 2 * t + e, live - 1);
+      limit[q][e] = visible_keys(A, kv, ql, (r0 + row) / A.G);
+      full = min(full, limit[q][e]);
+    }
+  }
+  full = min(full, __shfl_xor_sync(0xffffffffu, full, 1));
+  full = min(full, __shfl_xor_sync(0xffffffffu, full, 2));
+
+  float acc[NQ][NT][4];  // channels g D/8 + 2j (+ 1 from [2] on) of rows 2t + e
+  float m[NQ][2], l[NQ][2];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    m[q][0] = m[q][1] = -INFINITY;
+    l[q][0] = l[q][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[q][j][0] = acc[q][j][1] = acc[q][j][2] = acc[q][j][3] = 0.f;
+  }
 
   int stage = 0;
   for (int n = n0; n < hi; n += kStep) {
@@ -227,20 +259,28 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
     const uint8_t* vc = kc + F::kCodes;
     const float4* meta = reinterpret_cast<const float4*>(vc + F::kCodes);
     stage = stage == ST - 1 ? 0 : stage + 1;
-    // ---- scores
-    float sc[S / 8][4];
+    // ---- scores of tokens 16 f + g (+ 8 from [2] on) and rows 2t + e
+    float sc[NQ][HF][4];
 #pragma unroll
-    for (int nt = 0; nt < S / 8; ++nt) {
-      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+    for (int f = 0; f < HF; ++f) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) sc[q][f][0] = sc[q][f][1] = sc[q][f][2] = sc[q][f][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < KV; ++c) {
-        const uint4 r = *reinterpret_cast<const uint4*>(kc + slab_at<D>(nt * 8 + g, c * 4 + t));
+        const uint4 r0v = *reinterpret_cast<const uint4*>(kc + slab_at<D>(f * 16 + g, c * 4 + t));
+        const uint4 r8v =
+            *reinterpret_cast<const uint4*>(kc + slab_at<D>(f * 16 + g + 8, c * 4 + t));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t x = k == 0 ? r.x : k == 1 ? r.y : k == 2 ? r.z : r.w;
-          const uint32_t b0 = half2_of(x & 0xffffu), b1 = half2_of(x >> 16);
+          const uint32_t x = k == 0 ? r0v.x : k == 1 ? r0v.y : k == 2 ? r0v.z : r0v.w;
+          const uint32_t y = k == 0 ? r8v.x : k == 1 ? r8v.y : k == 2 ? r8v.z : r8v.w;
+          const uint32_t a[4] = {half2_of(x & 0xffffu), half2_of(y & 0xffffu), half2_of(x >> 16),
+                                 half2_of(y >> 16)};
 #pragma unroll
-          for (int p = QP - 1; p >= 0; --p) mma16816(sc[nt], qa[p][c * 4 + k], b0, b1);
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int p = QP - 1; p >= 0; --p)
+              mma16816(sc[q][f], a, qb[p][q][c * 4 + k][0], qb[p][q][c * 4 + k][1]);
         }
       }
     }
@@ -253,59 +293,68 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
       lv[f] = m4.z + (m4.y > 0.f ? log2f(m4.y) : 0.f);
       iv[f] = m4.y > 0.f ? 1.f / m4.y : 0.f;
     }
-    // ---- softmax of rows g (i = 0) and g + 8 (i = 1)
+    // ---- softmax of rows 2t (e = 0) and 2t + 1
     bool grew = false;
-    float alpha[2], mref[2];
+    float alpha[NQ][2], mref[NQ][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mx = -INFINITY;
+    for (int q = 0; q < NQ; ++q)
 #pragma unroll
-      for (int nt = 0; nt < S / 8; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        float mx = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = sc[nt][2 * i + e];
-          x = fmaf(x, mul[i] * kf[nt >> 1], lv[nt >> 1]);
-          if (n + nt * 8 + 2 * t + e >= limit[i]) x = -INFINITY;
-          mx = fmaxf(mx, x);
-        }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[i], mx);
-      mref[i] = mn == -INFINITY ? 0.f : mn - kShift;
-      alpha[i] = mn == -INFINITY ? 1.f : ex2_approx(m[i] - mn);
-      grew = grew || mn > m[i];
-      m[i] = mn;
-    }
+        for (int f = 0; f < HF; ++f)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float& x = sc[q][f][2 * i + e];
+            x = fmaf(x, mul[q][e] * kf[f], lv[f]);
+            if (n + S > full && n + f * 16 + g + 8 * i >= limit[q][e]) x = -INFINITY;
+            mx = fmaxf(mx, x);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m[q][e], mx);
+        mref[q][e] = mn == -INFINITY ? 0.f : mn - kShift;
+        alpha[q][e] = mn == -INFINITY ? 1.f : ex2_approx(m[q][e] - mn);
+        grew = grew || mn > m[q][e];
+        m[q][e] = mn;
+      }
     if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[j][0] *= alpha[0];
-        acc[j][1] *= alpha[0];
-        acc[j][2] *= alpha[1];
-        acc[j][3] *= alpha[1];
+      for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          acc[q][j][0] *= alpha[q][0];
+          acc[q][j][1] *= alpha[q][1];
+          acc[q][j][2] *= alpha[q][0];
+          acc[q][j][3] *= alpha[q][1];
+        }
+        l[q][0] *= alpha[q][0];
+        l[q][1] *= alpha[q][1];
       }
-      l[0] *= alpha[0];
-      l[1] *= alpha[1];
     }
     // ---- P and the output
 #pragma unroll
     for (int f = 0; f < HF; ++f) {
-      uint32_t pa[QP][4];
+      uint32_t pb[QP][NQ][2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // rows g, g + 8 of tokens 2t.., then of 8 + 2t..
-        const int i = q & 1, nt = 2 * f + (q >> 1);
-        float p0 = ex2_approx(sc[nt][2 * i] - mref[i]);
-        float p1 = ex2_approx(sc[nt][2 * i + 1] - mref[i]);
-        l[i] = fmaf(p0 + p1, iv[f] > 0.f ? iv[f] : 1.f, l[i]);
+      for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int p = 0; p < QP; ++p) {
-          const uint32_t h = pack_half2(p0, p1);
-          pa[p][q] = h;
-          const float2 y = unpack_half2(h);
-          p0 -= y.x;
-          p1 -= y.y;
+        for (int i = 0; i < 2; ++i) {  // tokens g, then g + 8
+          float p0 = ex2_approx(sc[q][f][2 * i] - mref[q][0]);
+          float p1 = ex2_approx(sc[q][f][2 * i + 1] - mref[q][1]);
+          const float u = iv[f] > 0.f ? iv[f] : 1.f;
+          l[q][0] = fmaf(p0, u, l[q][0]);
+          l[q][1] = fmaf(p1, u, l[q][1]);
+#pragma unroll
+          for (int p = 0; p < QP; ++p) {
+            const uint32_t h = pack_half2(p0, p1);
+            pb[p][q][i] = transpose8(h);
+            const float2 y = unpack_half2(h);
+            p0 -= y.x;
+            p1 -= y.y;
+          }
         }
-      }
       uint32_t vr[4][VW];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -318,32 +367,32 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
               *reinterpret_cast<const uint2*>(vc + slab_at<D>(row, g >> 1) + (g & 1) * 8);
           vr[i][0] = x.x, vr[i][1] = x.y;
         }
-        if (!(iv[f] > 0.f)) {
+      }
+      if (!(iv[f] > 0.f)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
-        }
       }
 #pragma unroll
-      for (int j = 0; j < NT; j += 4) {
-        // four channels of tokens (2t, 2t + 1) and (2t + 8, 2t + 9), as pairs
-        const uint32_t a0 = __byte_perm(vr[0][j >> 2], vr[1][j >> 2], 0x5140);
-        const uint32_t a1 = __byte_perm(vr[0][j >> 2], vr[1][j >> 2], 0x7362);
-        const uint32_t c0 = __byte_perm(vr[2][j >> 2], vr[3][j >> 2], 0x5140);
-        const uint32_t c1 = __byte_perm(vr[2][j >> 2], vr[3][j >> 2], 0x7362);
+      for (int j = 0; j < NT; ++j) {
+        // channels 2j and 2j + 1 of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
+        const uint32_t pick = j & 1 ? 0x7362 : 0x5140;
+        const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], pick);
+        const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], pick);
+        const uint32_t a[4] = {half2_of(x & 0xffffu), half2_of(x >> 16), half2_of(y & 0xffffu),
+                               half2_of(y >> 16)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t x = e < 2 ? a0 : a1, y = e < 2 ? c0 : c1;
-          const uint32_t b0 = half2_of((e & 1) ? x >> 16 : x & 0xffffu);
-          const uint32_t b1 = half2_of((e & 1) ? y >> 16 : y & 0xffffu);
+        for (int q = 0; q < NQ; ++q) {
           if constexpr (kF32) {
             // a sum of its own per slab: the long sum is then a rounded fp32 one
             float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int p = QP - 1; p >= 0; --p) mma16816(d, pa[p], b0, b1);
+            for (int p = QP - 1; p >= 0; --p) mma16816(d, a, pb[p][q][0], pb[p][q][1]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[j + e][c] += d[c];
+            for (int c = 0; c < 4; ++c) acc[q][j][c] += d[c];
           } else {
-            mma16816(acc[j + e], pa[0], b0, b1);
+            mma16816(acc[q][j], a, pb[0][q][0], pb[0][q][1]);
           }
         }
       }
@@ -353,27 +402,30 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   // ---- the CTA's warps, merged in their order; the rings are done with
   cp_async_wait<0>();
   __syncthreads();
-  float(*sm_o)[16][D + 4] = reinterpret_cast<float(*)[16][D + 4]>(smem);
-  float(*sm_ml)[16][2] = reinterpret_cast<float(*)[16][2]>(smem + kFewWarps * 16 * (D + 4) * 4);
+  float(*sm_o)[kTile][D + 4] = reinterpret_cast<float(*)[kTile][D + 4]>(smem);
+  float(*sm_ml)[kTile][2] =
+      reinterpret_cast<float(*)[kTile][2]>(smem + kFewWarps * kTile * (D + 4) * 4);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    if (t == 0) {
-      sm_ml[warp][g + 8 * i][0] = m[i] - kShift;
-      sm_ml[warp][g + 8 * i][1] = l[i];
+  for (int q = 0; q < NQ; ++q)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float& x = l[q][e];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      const int row = 8 * q + 2 * t + e;
+      if (g == 0) {
+        sm_ml[warp][row][0] = m[q][e] - kShift;
+        sm_ml[warp][row][1] = x;
+      }
+#pragma unroll
+      for (int j = 0; j < NT; j += 2)
+        *reinterpret_cast<float4*>(&sm_o[warp][row][g * (D / 8) + 2 * j]) = make_float4(
+            acc[q][j][e], acc[q][j][2 + e], acc[q][j + 1][e], acc[q][j + 1][2 + e]);
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int j = 0; j < NT; j += 4)
-        *reinterpret_cast<float4*>(&sm_o[warp][g + 8 * i][(2 * t + e) * (D / 8) + j]) =
-            make_float4(acc[j][2 * i + e], acc[j + 1][2 * i + e], acc[j + 2][2 * i + e],
-                        acc[j + 3][2 * i + e]);
-  }
   __syncthreads();
-  constexpr int TPR = kFewWarps * 32 / 16;  // threads per row
-  constexpr int W = D / TPR;                // channels per thread
+  constexpr int TPR = kFewWarps * 32 / kTile;  // threads per row
+  constexpr int W = D / TPR;                   // channels per thread
   const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * 4;
   if (row >= live) return;
   float M = -INFINITY, L = 0.f, out[W];
@@ -397,7 +449,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2)
   }
   const int r = r0 + row;
   if (w.part >= 0) {
-    const long long pr = w.part * kFewTile + row;
+    const long long pr = w.part * kTile + row;
 #pragma unroll
     for (int c = 0; c < W; c += 4)
       *reinterpret_cast<float4*>(A.part_o + pr * D + c0 + c * TPR) =
@@ -511,13 +563,16 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
   CachePlan p{};
   const long long rows = (long long)q.n_tokens * (q.heads / c.heads);
   const long long cap = (long long)c.max_pages * c.page_tokens;
-  p.tile = q.dtype == MMDIT_BF16 && rows > kFewRows ? kManyTile : kFewTile;
+  p.tile = q.dtype == MMDIT_BF16 && rows > kFewRows ? kManyTile : rows > 8 ? 16 : 8;
   p.tiles = (int)((rows + p.tile - 1) / p.tile);
   p.items = (long long)p.tiles * c.heads * q.batch;
-  if (p.tile == kFewTile) {
-    // Two CTAs of four warps per SM keep enough loads in flight; a range is at
-    // least 512 tokens (16 slabs for the CTA), or its merge costs more than it saves.
-    p.splits = (int)std::max(1LL, std::min(2 * 148 / p.items, (cap + 511) / 512));
+  if (p.tile != kManyTile) {
+    // A wave of three CTAs of four warps per SM (two where their registers fit no third); a
+    // range is at least 512 tokens (16 slabs for the CTA), or its merge costs more than it
+    // saves.
+    const int weight = q.head_dim * (p.tile / 8) * (q.dtype == MMDIT_F32 ? 2 : 1);
+    p.splits = (int)std::max(
+        1LL, std::min((weight >= 256 ? 2 : 3) * 148 / p.items, (cap + 511) / 512));
     p.whole = p.splits > 1 ? 0 : p.items;
   } else {
     // One CTA per SM.  What is left behind the whole waves is split so that its
@@ -541,17 +596,19 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
   return p;
 }
 
-template <typename T, int D>
+template <typename T, int D, int NQ>
 cudaError_t launch_few(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once_per_device(dev, [] {
-    return cudaFuncSetAttribute(cache_attn_few_kernel<T, D>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, Few<T, D>::kSmem);
+    return cudaFuncSetAttribute(cache_attn_few_kernel<T, D, NQ>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Few<T, D, NQ>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  cache_attn_few_kernel<T, D><<<(unsigned)p.grid(), kFewWarps * 32, Few<T, D>::kSmem, s>>>(A);
+  cache_attn_few_kernel<T, D, NQ>
+      <<<(unsigned)p.grid(), kFewWarps * 32, Few<T, D, NQ>::kSmem, s>>>(A);
   return cudaGetLastError();
 }
 template <typename T, int D>
@@ -573,7 +630,8 @@ cudaError_t launch_merge(const CacheAttnArgs& A, const CachePlan& p, cudaStream_
 template <typename T, int D>
 cudaError_t launch_cache_attn(const CacheAttnArgs& A, const CachePlan& p, cudaStream_t s) {
   cudaError_t e = p.tile == kManyTile ? launch_cache_attn_many(A, D, (unsigned)p.grid(), s)
-                                      : launch_few<T, D>(A, p, s);
+                  : p.tile == 16      ? launch_few<T, D, 2>(A, p, s)
+                                      : launch_few<T, D, 1>(A, p, s);
   if (e == cudaSuccess && p.whole < p.items) e = launch_merge<T, D>(A, p, s);
   return e;
 }
@@ -587,7 +645,7 @@ int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c) {
   if (q->heads % c->heads != 0)
     return fail(MMDIT_EINVAL, "cache_attn: %d query heads over %d K/V heads", q->heads, c->heads);
   const long long rows = (long long)q->n_tokens * (q->heads / c->heads) + kManyTile;
-  if (rows > 0x7fffffffLL || (rows / kFewTile + 1) * c->heads * q->batch > 0x7fffffffLL)
+  if (rows > 0x7fffffffLL || (rows / 16 + 1) * c->heads * q->batch > 0x7fffffffLL)
     return fail(MMDIT_EINVAL, "cache_attn: too many query rows");
   return MMDIT_OK;
 }

@@ -40,8 +40,9 @@ struct CacheAttnArgs {
   int* err;
 };
 
-constexpr int kFewTile = 16;    // rows per CTA: few rows, and every fp32 call (cache_attn.cu)
-constexpr int kManyTile = 256;  // many bf16 rows, on tcgen05 (cache_attn_tc.cu)
+// Rows per CTA: 8 or 16 (few rows, and every fp32 call: cache_attn.cu), or this (many
+// bf16 rows, on tcgen05: cache_attn_tc.cu).
+constexpr int kManyTile = 256;
 constexpr int kUnit = 128;      // tokens: granularity of the split key ranges
 
 __device__ __forceinline__ int held_tokens(const CacheAttnArgs& A, int b) {
