@@ -64,7 +64,10 @@ __device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
   }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(there ? 16 : 0)
                : "memory");
@@ -85,7 +88,7 @@ __device__ __forceinline__ void cp_async_wait() {
 template <typename T, int D, int NQ>
 struct Few {
   static constexpr bool kF32 = sizeof(T) == 4;
-  static constexpr int S = kF32 ? 16 : 32;  // tokens per slab
+  static constexpr int S = 32;  // tokens per slab
   static constexpr int kCtas = D * NQ * (kF32 ? 2 : 1) >= 256 ? 2 : 3;  // per SM, by registers
   static constexpr int kCodes = S * D;
   static constexpr int kStage = 2 * kCodes + 32;
@@ -106,6 +109,14 @@ __device__ __forceinline__ int slab_at(int r, int c) {
   else return (r >> 1) * 128 + ((((r & 1) << 2 | c) ^ (r & 6)) << 4);
 }
 
+// log2 of a normal x > 0: the exponent and the approximate logarithm of the mantissa,
+// which is good to 2^-22 there (of a large x it would be to 2^-22 of the result).
+__device__ __forceinline__ float log2_normal(float x) {
+  const int bits = __float_as_int(x);
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(__int_as_float((bits & 0x7fffff) | 0x3f800000)));
+  return (float)((bits >> 23) - 127) + y;
+}
 // 8 x 8 block of 16-bit values held as a fragment (row g, columns 2t, 2t + 1), transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -156,13 +167,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       const long long from = (page * A.page + ((n + 16 * f) & (A.page - 1))) * D + lane * 16;
       const uint8_t *kp = A.k + from, *vp = A.v + from;  // 16 D consecutive bytes
       const int rows = id[f] >= 0 ? hi - n - 16 * f : 0;
+      const uint32_t at[2] = {dst + f * 16 * D + place,
+                              dst + f * 16 * D + (D == 128 ? place ^ 64u : place)};
+      if (rows >= 16) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint32_t at =
-            dst + f * 16 * D + i * 512 + (D == 128 && (i & 1) ? place ^ 64u : place);
-        const bool there = (lane + 32 * i) / (D / 16) < rows;
-        cp_async16(at, there ? kp + i * 512 : A.k, there);
-        cp_async16(at + F::kCodes, there ? vp + i * 512 : A.v, there);
+        for (int i = 0; i < D / 32; ++i) {
+          cp_async16(at[i & 1] + i * 512, kp + i * 512);
+          cp_async16(at[i & 1] + i * 512 + F::kCodes, vp + i * 512);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const bool there = (lane + 32 * i) / (D / 16) < rows;
+          cp_async16_if(at[i & 1] + i * 512, there ? kp + i * 512 : A.k, there);
+          cp_async16_if(at[i & 1] + i * 512 + F::kCodes, there ? vp + i * 512 : A.v, there);
+        }
       }
       if (lane == f) {
         float* m = reinterpret_cast<float*>(to + 2 * F::kCodes) + 4 * f;
@@ -290,8 +309,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       const float4 m4 = meta[f];
       kf[f] = m4.x;
       // a page that is not there is not seen; a V scale of 0 stands for zeros
-      lv[f] = m4.z + (m4.y > 0.f ? log2f(m4.y) : 0.f);
-      iv[f] = m4.y > 0.f ? 1.f / m4.y : 0.f;
+      lv[f] = m4.z + (m4.y > 0.f ? log2_normal(m4.y) : 0.f);
+      iv[f] = m4.y > 0.f ? __frcp_rn(m4.y) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int f = 0; f < HF; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[q][f][i] = fmaf(sc[q][f][i], mul[q][i & 1] * kf[f], lv[f]);
+    if (__any_sync(0xffffffffu, n + S > full)) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int f = 0; f < HF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + f * 16 + g + 8 * (i >> 1) >= limit[q][i & 1]) sc[q][f][i] = -INFINITY;
     }
     // ---- softmax of rows 2t (e = 0) and 2t + 1
     bool grew = false;
@@ -305,10 +339,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         for (int f = 0; f < HF; ++f)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float& x = sc[q][f][2 * i + e];
-            x = fmaf(x, mul[q][e] * kf[f], lv[f]);
-            if (n + S > full && n + f * 16 + g + 8 * i >= limit[q][e]) x = -INFINITY;
-            mx = fmaxf(mx, x);
+            mx = fmaxf(mx, sc[q][f][2 * i + e]);
           }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
@@ -333,10 +364,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         l[q][1] *= alpha[q][1];
       }
     }
-    // ---- P and the output
+    // ---- P
+    uint32_t pb[HF][QP][NQ][2];
 #pragma unroll
-    for (int f = 0; f < HF; ++f) {
-      uint32_t pb[QP][NQ][2];
+    for (int f = 0; f < HF; ++f)
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -349,53 +380,63 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
 #pragma unroll
           for (int p = 0; p < QP; ++p) {
             const uint32_t h = pack_half2(p0, p1);
-            pb[p][q][i] = transpose8(h);
-            const float2 y = unpack_half2(h);
-            p0 -= y.x;
-            p1 -= y.y;
+            pb[f][p][q][i] = transpose8(h);
+            if (p + 1 < QP) {
+              const float2 y = unpack_half2(h);
+              p0 -= y.x;
+              p1 -= y.y;
+            }
           }
         }
-      uint32_t vr[4][VW];
+    // ---- the output
+    uint32_t vr[HF][4][VW];
+#pragma unroll
+    for (int f = 0; f < HF; ++f) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = f * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
         if constexpr (D == 128) {
           const uint4 x = *reinterpret_cast<const uint4*>(vc + slab_at<D>(row, g));
-          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][2] = x.z, vr[i][3] = x.w;
+          vr[f][i][0] = x.x, vr[f][i][1] = x.y, vr[f][i][2] = x.z, vr[f][i][3] = x.w;
         } else {
           const uint2 x =
               *reinterpret_cast<const uint2*>(vc + slab_at<D>(row, g >> 1) + (g & 1) * 8);
-          vr[i][0] = x.x, vr[i][1] = x.y;
+          vr[f][i][0] = x.x, vr[f][i][1] = x.y;
         }
       }
       if (!(iv[f] > 0.f)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int k = 0; k < VW; ++k) vr[i][k] = 0u;
+          for (int k = 0; k < VW; ++k) vr[f][i][k] = 0u;
       }
+    }
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+    for (int j = 0; j < NT; ++j) {
+      // fp32: a sum of its own per slab, so that the long sum is a rounded one (the
+      // tensor cores truncate)
+      float d[NQ][4];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) d[q][c] = kF32 ? 0.f : acc[q][j][c];
+#pragma unroll
+      for (int f = 0; f < HF; ++f) {
         // channels 2j and 2j + 1 of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
         const uint32_t pick = j & 1 ? 0x7362 : 0x5140;
-        const uint32_t x = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], pick);
-        const uint32_t y = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], pick);
+        const uint32_t x = __byte_perm(vr[f][0][j >> 1], vr[f][1][j >> 1], pick);
+        const uint32_t y = __byte_perm(vr[f][2][j >> 1], vr[f][3][j >> 1], pick);
         const uint32_t a[4] = {half2_of(x & 0xffffu), half2_of(x >> 16), half2_of(y & 0xffffu),
                                half2_of(y >> 16)};
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          if constexpr (kF32) {
-            // a sum of its own per slab: the long sum is then a rounded fp32 one
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-            for (int p = QP - 1; p >= 0; --p) mma16816(d, a, pb[p][q][0], pb[p][q][1]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[q][j][c] += d[c];
-          } else {
-            mma16816(acc[q][j], a, pb[0][q][0], pb[0][q][1]);
-          }
-        }
+          for (int p = QP - 1; p >= 0; --p) mma16816(d[q], a, pb[f][p][q][0], pb[f][p][q][1]);
       }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[q][j][c] = kF32 ? acc[q][j][c] + d[q][c] : d[q][c];
     }
   }
 
