@@ -13,7 +13,7 @@
 //
 // Copy.  The page lists travel in the kernel's parameters: no list has to be
 // copied to the device first, and one launch moves up to kCopyPairs pages.
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 #include <limits.h>
 
 #include <algorithm>
@@ -108,14 +108,25 @@ __device__ __forceinline__ float inverse_pow2(float s) {  // s = 2^e, e in -60..
 }
 __device__ __forceinline__ bool is_number(float x) { return fabsf(x) <= 3.402823466e38f; }
 
+// Four values as e4m3 codes, to nearest, clipped to +-448; and the values of four codes.
+// As 32-bit registers: the 16-bit halves of the type's C++ interface cost more than the
+// conversions.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
-__device__ __forceinline__ float2 value2(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+__device__ __forceinline__ void values4(uint32_t codes, float2& a, float2& b) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+  a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
 }
 
 // the values of one 16-byte vector
@@ -180,7 +191,8 @@ __device__ __forceinline__ void rescale_codes(uint8_t* codes, int n, float f, in
                                               int threads) {
   uint32_t* w = reinterpret_cast<uint32_t*>(codes);
   for (int i = tid; i < n / 4; i += threads) {
-    const float2 a = value2(w[i] & 0xffffu), c = value2(w[i] >> 16);
+    float2 a, c;
+    values4(w[i], a, c);
     w[i] = codes4(a.x * f, a.y * f, c.x * f, c.y * f);
   }
 }

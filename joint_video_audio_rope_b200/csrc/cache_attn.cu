@@ -89,7 +89,7 @@ template <typename T, int D, int NQ>
 struct Few {
   static constexpr bool kF32 = sizeof(T) == 4;
   static constexpr int S = 32;  // tokens per slab
-  static constexpr int kCtas = D * NQ * (kF32 ? 2 : 1) >= 256 ? 2 : 3;  // per SM, by registers
+  static constexpr int kCtas = D * NQ * (kF32 ? 2 : 1) > 256 ? 2 : 3;  // per SM, by registers
   static constexpr int kCodes = S * D;
   static constexpr int kStage = 2 * kCodes + 32;
   static constexpr int kFit = 222 * 1024 / (kCtas * kFewWarps * kStage);
@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         for (int k = 0; k < 4; ++k) {
           const uint32_t x = k == 0 ? r0v.x : k == 1 ? r0v.y : k == 2 ? r0v.z : r0v.w;
           const uint32_t y = k == 0 ? r8v.x : k == 1 ? r8v.y : k == 2 ? r8v.z : r8v.w;
-          const uint32_t a[4] = {half2_of(x & 0xffffu), half2_of(y & 0xffffu), half2_of(x >> 16),
-                                 half2_of(y >> 16)};
+          uint32_t a[4];
+          halves_of(x, a[0], a[2]);
+          halves_of(y, a[1], a[3]);
 #pragma unroll
           for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -426,8 +427,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         const uint32_t pick = j & 1 ? 0x7362 : 0x5140;
         const uint32_t x = __byte_perm(vr[f][0][j >> 1], vr[f][1][j >> 1], pick);
         const uint32_t y = __byte_perm(vr[f][2][j >> 1], vr[f][3][j >> 1], pick);
-        const uint32_t a[4] = {half2_of(x & 0xffffu), half2_of(x >> 16), half2_of(y & 0xffffu),
-                               half2_of(y >> 16)};
+        uint32_t a[4];
+        halves_of(x, a[0], a[1]);
+        halves_of(y, a[2], a[3]);
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -613,7 +615,7 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
     // saves.
     const int weight = q.head_dim * (p.tile / 8) * (q.dtype == MMDIT_F32 ? 2 : 1);
     p.splits = (int)std::max(
-        1LL, std::min((weight >= 256 ? 2 : 3) * 148 / p.items, (cap + 511) / 512));
+        1LL, std::min((weight > 256 ? 2 : 3) * 148 / p.items, (cap + 511) / 512));
     p.whole = p.splits > 1 ? 0 : p.items;
   } else {
     // One CTA per SM.  What is left behind the whole waves is split so that its

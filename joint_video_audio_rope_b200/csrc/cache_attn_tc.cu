@@ -34,7 +34,7 @@ constexpr int kPageSlots = 8;             // tiles whose pages and scales are he
 constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
 constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
 // registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
-constexpr int kRegsSoftmax = 184, kRegsConvert = 96, kRegsMma = 48;
+constexpr int kRegsSoftmax = 184, kRegsConvert = 104, kRegsMma = 40;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 512, "register split");
 
 template <int D>
@@ -299,10 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = cw * 32 + i * RS + row;
         uint8_t* line = tile + half * kHalf + n * 128;
         uint4 a, b;
-        a.x = half2_of(r[i].x & 0xffffu), a.y = half2_of(r[i].x >> 16);
-        a.z = half2_of(r[i].y & 0xffffu), a.w = half2_of(r[i].y >> 16);
-        b.x = half2_of(r[i].z & 0xffffu), b.y = half2_of(r[i].z >> 16);
-        b.z = half2_of(r[i].w & 0xffffu), b.w = half2_of(r[i].w >> 16);
+        halves_of(r[i].x, a.x, a.y);
+        halves_of(r[i].y, a.z, a.w);
+        halves_of(r[i].z, b.x, b.y);
+        halves_of(r[i].w, b.z, b.w);
         *reinterpret_cast<uint4*>(line + (((2 * c4) ^ (n & 7)) << 4)) = a;
         *reinterpret_cast<uint4*>(line + (((2 * c4 + 1) ^ (n & 7)) << 4)) = b;
       }
