@@ -35,9 +35,11 @@ namespace {
 constexpr int kFewWarps = 4;
 // bf16 rows per (item, K/V head) up to which 16-row tiles are taken
 constexpr int kFewRows = 16;
-// The largest probability of a row is held as 2^14: fp16 keeps its relative
-// precision down to 2^-14, so what is 2^-28 of the largest is still whole.
+// The probability of a row's reference maximum is held as 2^14: fp16 keeps its relative
+// precision down to 2^-14, so what is 2^-28 of it is still whole.  The reference may be
+// behind the maximum by a factor of two (2^15 is still a number in fp16).
 constexpr float kShift = 14.f;
+constexpr float kGrow = 1.f;
 
 __device__ __forceinline__ float2 unpack_half2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -255,10 +257,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
   full = min(full, __shfl_xor_sync(0xffffffffu, full, 2));
 
   float acc[NQ][NT][4];  // channels g D/8 + 2j (+ 1 from [2] on) of rows 2t + e
-  float m[NQ][2], l[NQ][2];
+  float m[NQ][2], l[NQ][2], mref[NQ][2];  // reference maxima, sums; m - kShift (0: none yet)
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     m[q][0] = m[q][1] = -INFINITY;
+    mref[q][0] = mref[q][1] = 0.f;
     l[q][0] = l[q][1] = 0.f;
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[q][j][0] = acc[q][j][1] = acc[q][j][2] = acc[q][j][3] = 0.f;
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         }
       }
     }
-    float kf[HF], lv[HF], iv[HF];
+    float kf[HF], lv[HF], iv[HF], wv[HF];
 #pragma unroll
     for (int f = 0; f < HF; ++f) {
       const float4 m4 = meta[f];
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       // a page that is not there is not seen; a V scale of 0 stands for zeros
       lv[f] = m4.z + (m4.y > 0.f ? log2_normal(m4.y) : 0.f);
       iv[f] = m4.y > 0.f ? __frcp_rn(m4.y) : 0.f;
+      wv[f] = m4.y > 0.f ? iv[f] : 1.f;
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
@@ -328,41 +332,43 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
           for (int i = 0; i < 4; ++i)
             if (n + f * 16 + g + 8 * (i >> 1) >= limit[q][i & 1]) sc[q][f][i] = -INFINITY;
     }
-    // ---- softmax of rows 2t (e = 0) and 2t + 1
+    // ---- softmax of rows 2t (e = 0) and 2t + 1: the reference moves once a score is beyond
+    // twice it, which few slabs need, so lanes seldom have to agree on a maximum
     bool grew = false;
-    float alpha[NQ][2], mref[NQ][2];
+    float top[NQ][2];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = -INFINITY;
+        float mx = sc[q][0][e];
 #pragma unroll
-        for (int f = 0; f < HF; ++f)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx = fmaxf(mx, sc[q][f][2 * i + e]);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m[q][e], mx);
-        mref[q][e] = mn == -INFINITY ? 0.f : mn - kShift;
-        alpha[q][e] = mn == -INFINITY ? 1.f : ex2_approx(m[q][e] - mn);
-        grew = grew || mn > m[q][e];
-        m[q][e] = mn;
+        for (int f = 0; f < HF; ++f) mx = max3f(mx, sc[q][f][e], sc[q][f][2 + e]);
+        top[q][e] = mx;
+        grew = grew || mx > m[q][e] + kGrow;
       }
     if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = top[q][e];
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m[q][e], mx);
+          alpha[e] = mn == -INFINITY ? 1.f : ex2_approx(m[q][e] - mn);
+          m[q][e] = mn;
+          mref[q][e] = mn == -INFINITY ? 0.f : mn - kShift;
+          l[q][e] *= alpha[e];
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          acc[q][j][0] *= alpha[q][0];
-          acc[q][j][1] *= alpha[q][1];
-          acc[q][j][2] *= alpha[q][0];
-          acc[q][j][3] *= alpha[q][1];
+          acc[q][j][0] *= alpha[0];
+          acc[q][j][1] *= alpha[1];
+          acc[q][j][2] *= alpha[0];
+          acc[q][j][3] *= alpha[1];
         }
-        l[q][0] *= alpha[q][0];
-        l[q][1] *= alpha[q][1];
       }
     }
     // ---- P
@@ -375,9 +381,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
         for (int i = 0; i < 2; ++i) {  // tokens g, then g + 8
           float p0 = ex2_approx(sc[q][f][2 * i] - mref[q][0]);
           float p1 = ex2_approx(sc[q][f][2 * i + 1] - mref[q][1]);
-          const float u = iv[f] > 0.f ? iv[f] : 1.f;
-          l[q][0] = fmaf(p0, u, l[q][0]);
-          l[q][1] = fmaf(p1, u, l[q][1]);
+          l[q][0] = fmaf(p0, wv[f], l[q][0]);
+          l[q][1] = fmaf(p1, wv[f], l[q][1]);
 #pragma unroll
           for (int p = 0; p < QP; ++p) {
             const uint32_t h = pack_half2(p0, p1);
