@@ -350,14 +350,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q rows of this warp: fp16, largest value at 2^14..2^15
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
         const int c = lane % LPR;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += RPI) {
-          const int n = warp * 32 + i + lane / LPR, r = w.r0 + n;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        uint4 rows[32 / RPI];  // all loads at once
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int n = warp * 32 + i * RPI + lane / LPR, r = w.r0 + n;
+          rows[i] = make_uint4(0u, 0u, 0u, 0u);
           if (n < w.live)
-            v = *reinterpret_cast<const uint4*>(
+            rows[i] = *reinterpret_cast<const uint4*>(
                 (const __nv_bfloat16*)A.q + w.b * A.q_sb + (long long)(r / A.G) * A.q_st +
                 (long long)(w.hk * A.G + r % A.G) * D + c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int n = warp * 32 + i * RPI + lane / LPR;
+          uint4 v = rows[i];
           const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
           float2 x[4];
           float am = 0.f;
@@ -512,11 +518,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
           if (w.part >= 0) {
-            if (valid) {
+            // 32 rows x 32 channels through shared memory: whole 128-byte runs leave
+            __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<uint4*>(A.part_o + pr * D + c * 32 + i) =
-                    make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int n = i * 4 + (lane >> 3), rr = warp * 32 + n;
+              if (rr < w.live)
+                *reinterpret_cast<uint4*>(A.part_o + (w.part * kManyTile + rr) * D + c * 32 +
+                                          (lane & 7) * 4) =
+                    *reinterpret_cast<const uint4*>(stage + n * 128 +
+                                                    (((lane & 7) ^ (n & 7)) << 4));
             }
           } else {
 #pragma unroll
