@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "rotary.cuh"
@@ -143,6 +144,21 @@ __device__ __forceinline__ void values_of(const uint4& r, float (&x)[4], float*)
   const float* p = reinterpret_cast<const float*>(&r);
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = p[i];
+}
+
+// the values of one 16-byte vector times a power of two (exact in bf16 too: what falls
+// below its subnormals is far below the smallest code)
+__device__ __forceinline__ void scaled_values(uint4 r, float f, float (&x)[8], __nv_bfloat16*) {
+  __nv_bfloat162* p = reinterpret_cast<__nv_bfloat162*>(&r);
+  const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = __hmul2(p[i], f2);
+  values_of(r, x, (__nv_bfloat16*)nullptr);
+}
+__device__ __forceinline__ void scaled_values(const uint4& r, float f, float (&x)[4], float*) {
+  values_of(r, x, (float*)nullptr);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] *= f;
 }
 
 // Maxima that a NaN wins.  Non-negative values order as their bits do, infinity and
@@ -288,24 +304,29 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 
   constexpr uint32_t kInf = 0x7f800000u;
   const int h0 = blockIdx.y * A.slice, h1 = min(C.heads, h0 + A.slice);
+  // WHOLE: every row of the page is new, which spares the rows' checks.
+  auto store_heads = [&](auto whole) {
+  constexpr bool WHOLE = decltype(whole)::value;
+  auto live = [&](int row) { return WHOLE || (row >= r_lo && row < r_hi); };
   for (int h = h0; h < h1; ++h) {
     const int par = (h - h0) & 1;
-    const long long from = b * A.sb + tok0 * A.st + (long long)h * D + chunk * E;
+    const long long from = b * A.sb + (tok0 + row0) * A.st + (long long)h * D + chunk * E;
+    const long long step = rstep * A.st;
+    const T *kp = (const T*)A.k + from, *vp = (const T*)A.v + from;
     uint4 kr[NV], vr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int row = row0 + i * rstep;
-      kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row >= r_lo && row < r_hi) {
-        kr[i] = __ldcs(reinterpret_cast<const uint4*>((const T*)A.k + from + row * A.st));
-        vr[i] = __ldcs(reinterpret_cast<const uint4*>((const T*)A.v + from + row * A.st));
+      if (!WHOLE) kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live(row0 + i * rstep)) {
+        kr[i] = __ldcs(reinterpret_cast<const uint4*>(kp + i * step));
+        vr[i] = __ldcs(reinterpret_cast<const uint4*>(vp + i * step));
       }
     }
     const long long ph = (long long)id * C.heads + h;
     uint8_t* kc = (uint8_t*)C.k + ph * page * D;
     uint8_t* vc = (uint8_t*)C.v + ph * page * D;
     float old_k = 0.f, old_v = 0.f;
-    if (r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
+    if (!WHOLE && r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
 
     // ---- K turned: interleaved pairs in kx, half pairs in the tile; the largest |x|
     float kx[MODE == 1 ? NV * E : 1];
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
         const int row = row0 + i * rstep;
         // rows without a new token hold zeros; their angles are not there
         const float4* a = reinterpret_cast<const float4*>(
-            angles + min(max(row, r_lo), r_hi - 1) * (D / 2)) + chunk;
+            angles + (WHOLE ? row : min(max(row, r_lo), r_hi - 1)) * (D / 2)) + chunk;
         float4 two;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
@@ -407,10 +428,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * rstep;
-        if (row < r_lo || row >= r_hi) continue;
+        if (!live(row)) continue;
         bool ok = keep_numbers(vr[i], (T*)nullptr);
         mv = vector_max(vr[i], mv, (T*)nullptr);
-        uint4 raw = *reinterpret_cast<const uint4*>((const T*)A.k + from + row * A.st);
+        uint4 raw = *reinterpret_cast<const uint4*>(kp + i * step);
         ok = keep_numbers(raw, (T*)nullptr) && ok;
         if (!ok) atomicOr(&lost[row >> 5], 1u << (row & 31));
         float x[E];
@@ -424,7 +445,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 
     // ---- scales; every thread has read the old ones before that barrier
     float sv = fit_scale(__uint_as_float(mv)), sk = fit_scale(__uint_as_float(mk));
-    if (r_lo > 0) {
+    if (!WHOLE && r_lo > 0) {
       sv = fmaxf(sv, floor_scale(old_v));
       sk = fmaxf(sk, floor_scale(old_k));
       if (sv > old_v) rescale_codes(vc, r_lo * D, old_v / sv, tid, threads);
@@ -440,18 +461,24 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int row = row0 + i * rstep;
-      if (row < r_lo || row >= r_hi) continue;
+      if (!live(row)) continue;
       const int to = row * D + chunk * E;
       uint32_t w[E / 4], v[E / 4];
       float x[E];
-      values_of(vr[i], x, (T*)nullptr);
+      scaled_values(vr[i], iv, x, (T*)nullptr);
 #pragma unroll
       for (int j = 0; j < E / 4; ++j)
-        v[j] = codes4(x[4 * j] * iv, x[4 * j + 1] * iv, x[4 * j + 2] * iv, x[4 * j + 3] * iv);
-      turned(i, x);
+        v[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+      if constexpr (MODE == 0) {
+        scaled_values(kr[i], ik, x, (T*)nullptr);
+      } else {
+        turned(i, x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) x[j] *= ik;
+      }
 #pragma unroll
       for (int j = 0; j < E / 4; ++j)
-        w[j] = codes4(x[4 * j] * ik, x[4 * j + 1] * ik, x[4 * j + 2] * ik, x[4 * j + 3] * ik);
+        w[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
       if (careful && ((lost[row >> 5] >> (row & 31)) & 1u)) {
 #pragma unroll
         for (int j = 0; j < E / 4; ++j) w[j] = 0x7f7f7f7fu;
@@ -465,6 +492,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
       }
     }
   }
+  };
+  if (r_lo == 0 && r_hi == page) store_heads(std::true_type{});
+  else store_heads(std::false_type{});
 }
 
 template <typename T, int MODE, int NV, int MAXT>
