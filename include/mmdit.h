@@ -567,7 +567,8 @@ typedef struct {
  *   place of such values of V: rows that attend to it give NaN, and no others.
  *   Every other slot of every page stays as it was.  Tokens at positions
  *   outside 0 .. capacity - 1, or whose page id is outside 0 .. n_pages - 1, are not
- *   stored.  No two items may append to the same page in one call.
+ *   stored.  No page may receive tokens at two places of the table in one call, and
+ *   k and v may not overlap the cache.
  *   Errors : EINVAL, EUNSUPPORTED, ECUDA.
  */
 MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tensor_desc* desc,

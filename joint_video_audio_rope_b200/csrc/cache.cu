@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
     if (!WHOLE && r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
 
     // ---- K turned: interleaved pairs in kx, half pairs in the tile; the largest |x|
-    float kx[MODE == 1 ? NV * E : 1];
+    [[maybe_unused]] float kx[MODE == 1 ? NV * E : 1];
     uint32_t mv = 0u, mk = 0u;
     if constexpr (MODE == 2) {
 #pragma unroll
@@ -511,7 +511,7 @@ cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
                                 128 * 128 * 4 * MODE);
   });
   if (e != cudaSuccess) return e;
-  const int pages = (A.N + page - 2) / page + 1;  // most pages that N tokens touch
+  const int pages = (int)((A.N + page - 2LL) / page) + 1;  // most pages that N tokens touch
   // Slices of the heads, one CTA each: a CTA takes as long as its heads and about two
   // more for the page's look-ups and angles, and about 768 threads fit an SM; the number of
   // slices with the shortest waves is taken (480p clip, bf16, interleaved: 136 us with 4

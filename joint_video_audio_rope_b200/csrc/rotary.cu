@@ -175,6 +175,7 @@ cudaError_t launch_rotary(RotaryArgs& A, int batch, int dtype, cudaStream_t s) {
   const long long blocks = ((long long)A.N + tpb - 1) / tpb * batch;
   const long long want = blocks * A.heads / (4 * 148);
   A.slice = (int)std::max(1LL, std::min<long long>(A.heads, want));
+  A.slice = std::max(A.slice, (A.heads + 65534) / 65535);
   if (A.slice > kUnroll) A.slice = (A.slice + kUnroll - 1) / kUnroll * kUnroll;
   const dim3 grid((A.N + tpb - 1) / tpb, (A.heads + A.slice - 1) / A.slice, batch);
   if (dtype == MMDIT_BF16) {

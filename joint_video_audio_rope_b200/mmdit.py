@@ -212,6 +212,14 @@ def _current_stream() -> int:
     return _current_stream()
 
 
+def _current_device() -> int:
+    global _current_device
+    import torch
+    torch.cuda.init()
+    _current_device = torch._C._cuda_getDevice
+    return _current_device()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         return _current_stream()
@@ -432,14 +440,44 @@ def rotary_params(theta: float, dim_t: int, dim_h: int = 0, dim_w: int = 0,
                         beta_fast, beta_slow, magnitude)
 
 
+def _here(*tensors) -> list:
+    """Addresses of tensors that must live on the current device (ints and None pass as they are)."""
+    out, current = [], None
+    for x in tensors:
+        if x is not None and not isinstance(x, int):
+            device = x.get_device()
+            if current is None and device >= 0:
+                current = _current_device()
+            if device < 0 or device != current:
+                raise ValueError(f"a tensor on {x.device} in a call on the current CUDA device")
+            x = x.data_ptr()
+        out.append(x)
+    return out
+
+
+_I32, _FLOAT = range(2)
+
+
+def _array(x, kind: int, n: int, what: str) -> None:
+    """Checks a packed per-item (or per-row) array of int32 or float32 (_I32, _FLOAT); ints and None pass."""
+    if x is None or isinstance(x, int):
+        return
+    import torch
+    if x.dtype is not (torch.int32 if kind == _I32 else torch.float32) or x.numel() != n or \
+            not x.is_contiguous():
+        raise ValueError(f"{what}: expected {n} packed values of {'int32' if kind == _I32 else 'float32'}")
+
+
 def rotary(q, q_out, q_desc, q_out_desc, k, k_out, k_desc, k_out_desc, layout: Layout,
            params: RotaryParams, first=None, transpose: bool = False, stream=None) -> None:
     """q_out = R q and k_out = R k (transpose: R^T, the gradient) at the positions of the
-    layout's tokens first[b] + n; q or k may be None with its three companions."""
-    _check(_lib.mmdit_rotary(_ptr(q), _ptr(q_out), q_desc, q_out_desc, _ptr(k),
-                             _ptr(k_out), k_desc, k_out_desc, layout,
-                             params, _ptr(first), 1 if transpose else 0,
-                             _stream(stream)))
+    layout's tokens first[b] + n (int32 [B] on the device; None: 0); q or k may be None with its
+    three companions."""
+    desc = q_desc if q_desc is not None else k_desc
+    _array(first, _I32, desc.batch if desc is not None else 0, "first")
+    q, q_out, k, k_out, first = _here(q, q_out, k, k_out, first)
+    _check(_lib.mmdit_rotary(q, q_out, q_desc, q_out_desc, k, k_out, k_desc, k_out_desc, layout,
+                             params, first, 1 if transpose else 0, _stream(stream)))
 
 
 def make_cache(k, v, k_scale, v_scale, page_table=None) -> Cache:
@@ -458,8 +496,13 @@ def make_cache(k, v, k_scale, v_scale, page_table=None) -> Cache:
         if page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous():
             raise ValueError("expected a packed int32 page table [batch, max_pages]")
         batch, per = page_table.shape
-    return Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1],
-                 k.shape[2], k.shape[3], _ptr(page_table), batch, per)
+    arrays = [x for x in (k, v, k_scale, v_scale, page_table) if x is not None]
+    if any(x.device != k.device for x in arrays):
+        raise ValueError("the arrays of a cache live on one device")
+    cache = Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1],
+                  k.shape[2], k.shape[3], _ptr(page_table), batch, per)
+    cache.codes = k  # the device of the handle, for the calls' checks
+    return cache
 
 
 def cache_append(k, v, desc: TensorDesc, cache: Cache, start, count=None,
@@ -467,8 +510,11 @@ def cache_append(k, v, desc: TensorDesc, cache: Cache, start, count=None,
                  stream=None) -> None:
     """Stores tokens start[b] .. start[b] + count[b] - 1 (int32 [B] on the device; count None:
     all N) in 8 bits; with layout and rotation, K is turned on the way."""
-    _check(_lib.mmdit_cache_append(_ptr(k), _ptr(v), desc, cache, _ptr(start),
-                                   _ptr(count), layout, rotation, _stream(stream)))
+    _array(start, _I32, desc.batch, "start")
+    _array(count, _I32, desc.batch, "count")
+    k, v, start, count, _ = _here(k, v, start, count, getattr(cache, "codes", None))
+    _check(_lib.mmdit_cache_append(k, v, desc, cache, start, count, layout, rotation,
+                                   _stream(stream)))
 
 
 def cache_attn_workspace_size(q_desc: TensorDesc, cache: Cache) -> int:
@@ -479,11 +525,15 @@ def cache_attn(q, o, q_desc: TensorDesc, o_desc: TensorDesc, cache: Cache, kv_le
                q_len=None, causal_block: int = 0, lse=None, workspace=None, ws_bytes: int = 0,
                stream=None) -> None:
     """o = softmax(q K^T * scale) V over the first kv_len[b] cached tokens (int32 [B] on the
-    device); causal_block = c: a row sees its own and earlier blocks of c tokens.  Workspace from
-    cache_attn_workspace_size."""
-    _check(_lib.mmdit_cache_attn(_ptr(q), _ptr(o), q_desc, o_desc,
-                                 cache, _ptr(kv_len), _ptr(q_len), causal_block, scale,
-                                 _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+    device); causal_block = c: a row sees its own and earlier blocks of c tokens.  lse: float
+    [B, heads, N].  Workspace from cache_attn_workspace_size."""
+    _array(kv_len, _I32, q_desc.batch, "kv_len")
+    _array(q_len, _I32, q_desc.batch, "q_len")
+    _array(lse, _FLOAT, q_desc.batch * q_desc.heads * q_desc.n_tokens, "lse")
+    q, o, kv_len, q_len, lse, workspace, _ = _here(q, o, kv_len, q_len, lse, workspace,
+                                                   getattr(cache, "codes", None))
+    _check(_lib.mmdit_cache_attn(q, o, q_desc, o_desc, cache, kv_len, q_len, causal_block, scale,
+                                 lse, workspace, ws_bytes, _stream(stream)))
 
 
 def cache_copy_pages(cache: Cache, src: Sequence[int], dst: Sequence[int], stream=None) -> None:
@@ -491,6 +541,7 @@ def cache_copy_pages(cache: Cache, src: Sequence[int], dst: Sequence[int], strea
     n = len(src)
     if len(dst) != n:
         raise ValueError("src and dst differ in length")
+    _here(getattr(cache, "codes", None))
     src, dst = array("i", src), array("i", dst)  # C int32, an eighth of a ctypes array's time
     _check(_lib.mmdit_cache_copy_pages(cache, n, src.buffer_info()[0], dst.buffer_info()[0],
                                        _stream(stream)))

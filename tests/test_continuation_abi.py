@@ -147,3 +147,26 @@ def test_make_cache_checks_its_tensors():
                 (k.transpose(1, 2), k.transpose(1, 2), s, s, t)):
         with pytest.raises(ValueError):
             M.make_cache(*bad)
+
+
+def test_tensors_elsewhere_and_arrays_of_another_shape_are_refused():
+    torch = pytest.importorskip("torch")
+    d, c = _desc(), _cache()
+    i32 = torch.zeros(2, dtype=torch.int32)
+    x = torch.zeros((2, 40, 4, 128), dtype=torch.bfloat16)
+    for call in (lambda: M.cache_append(x, 7 * FAKE, d, c, FAKE, stream=0),
+                 lambda: M.cache_append(6 * FAKE, 7 * FAKE, d, c, i32, stream=0),
+                 lambda: M.cache_append(6 * FAKE, 7 * FAKE, d, c, i32.long(), stream=0),
+                 lambda: M.cache_append(6 * FAKE, 7 * FAKE, d, c, FAKE, count=i32[:1], stream=0),
+                 lambda: M.cache_attn(6 * FAKE, 7 * FAKE, d, d, c, i32, 0.1, stream=0),
+                 lambda: M.cache_attn(6 * FAKE, 7 * FAKE, d, d, c, FAKE, 0.1, lse=torch.zeros((2, 4, 39)), stream=0),
+                 lambda: M.cache_attn(x, 7 * FAKE, d, d, c, FAKE, 0.1, stream=0),
+                 lambda: M.rotary(x, FAKE, d, d, None, None, None, None, _layout(), M.rotary_params(1e4, 64), stream=0),
+                 lambda: M.rotary(FAKE, 2 * FAKE, d, d, None, None, None, None, _layout(), M.rotary_params(1e4, 64),
+                                  first=i32.repeat(2), stream=0)):
+        with pytest.raises(ValueError):
+            call()
+    k = torch.zeros((3, 2, 16, 64), dtype=torch.uint8)
+    host = M.make_cache(k, k.clone(), torch.zeros((3, 2)), torch.zeros((3, 2)))
+    with pytest.raises(ValueError):
+        M.cache_copy_pages(host, [0], [1], stream=0)

@@ -624,6 +624,40 @@ def test_two_calls_at_once_with_a_workspace_each(M):
         assert all(torch.equal(a, b) for a, b in zip(alone, got))
 
 
+@pytest.mark.parametrize("dtype,N", [("bf16", 3), ("f32", 20), ("bf16", 90)])
+def test_split_calls_in_two_graphs(M, dtype, N):
+    """Long histories are split into key ranges and merged by a second kernel: two captured calls with a workspace
+    each, replayed together and in either order, give what the plain call gives, for each length of the history."""
+    rng = np.random.default_rng(45)
+    host, dev, cache = _new_cache(M, rng, 330, 2, 16, 64, 2, 150)
+    for d, h in zip(dev, host[:2]):
+        h[h & 127 == 127] = 3
+        d.copy_(torch.from_numpy(h))
+    kv = torch.tensor([2400, 1111], dtype=torch.int32, device="cuda")
+    runs = []
+    for i in range(2):
+        q, _ = _tensor(rng, (2, N, 6, 64), dtype)
+        o = torch.zeros_like(q)
+        n = M.cache_attn_workspace_size(M.desc_of(q), cache)
+        assert n > 0
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            M.cache_attn(q, o, M.desc_of(q), M.desc_of(o), cache, kv, 0.01, causal_block=1, workspace=ws, ws_bytes=n)
+        runs.append((q, o, graph, ws))
+    streams = [torch.cuda.Stream() for _ in runs]
+    for lengths in ([2400, 1111], [N, 2400], [17, 0], [2399, 2400]):
+        kv.copy_(torch.tensor(lengths, dtype=torch.int32))
+        want = [_attend(M, q, dev, cache, kv, None, 1, 0.01)[0] for q, *_ in runs]
+        torch.cuda.synchronize()
+        for order in (0, 1):
+            for r, s in list(zip(runs, streams))[::1 if order else -1]:
+                with torch.cuda.stream(s):
+                    r[2].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(w, r[1]) for w, r in zip(want, runs))
+
+
 def test_empty_calls(M):
     host, dev, cache = _new_cache(M, np.random.default_rng(44), 4, 2, 16, 64, 1, 2)
     q = torch.empty((1, 0, 2, 64), device="cuda")
