@@ -253,8 +253,6 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
   const long long p = lo / page + blockIdx.x;
   if (cnt <= 0 || p * page >= hi) return;
   const int id = C.page_table[(long long)b * C.max_pages + p];
-  MMDIT_DCHECK(id >= 0 && id < C.n_pages, A.err);
-  if (id < 0 || id >= C.n_pages) return;
   const int r_lo = (int)(max(lo, p * page) - p * page);  // new rows of the page
   const int r_hi = (int)(min(hi, (p + 1) * page) - p * page);
   const long long tok0 = p * page - start;               // input token of row 0
@@ -301,6 +299,10 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
     cluster_arrive();
     cluster_wait();
   }
+
+  // the page's id is first needed here: its load ran under the work on the angles
+  MMDIT_DCHECK(id >= 0 && id < C.n_pages, A.err);
+  if (id < 0 || id >= C.n_pages) return;
 
   constexpr uint32_t kInf = 0x7f800000u;
   const int h0 = blockIdx.y * A.slice, h1 = min(C.heads, h0 + A.slice);
