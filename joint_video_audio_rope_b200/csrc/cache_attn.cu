@@ -33,8 +33,9 @@ namespace mmdit {
 namespace {
 
 constexpr int kFewWarps = 4;
-// bf16 rows per (item, K/V head) up to which 16-row tiles are taken
-constexpr int kFewRows = 16;
+// bf16 rows per (item, K/V head) up to which tiles of 8 or 16 rows are taken: 24 heads over
+// 32,760 tokens, 32 rows: 78 us as two tiles, 84 on tcgen05; 48 rows: 105 and 85.
+constexpr int kFewRows = 32;
 // The probability of a row's reference maximum is held as 2^14: fp16 keeps its relative
 // precision down to 2^-14, so what is 2^-28 of it is still whole.  The reference may be
 // behind the maximum by a factor of two (2^15 is still a number in fp16).
