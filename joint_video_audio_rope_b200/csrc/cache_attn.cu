@@ -22,6 +22,10 @@
 // to 2^-29 of that; fp32 values are split into two fp16 parts (22 bits), and so
 // are the probabilities of an fp32 call.  Each warp runs its own softmax; the CTA's
 // warps, then the key ranges, are merged at the end in a fixed order.
+// One B200: 1 token of 24 heads over 75,600 tokens of 24 K/V heads (464 MB) 80 us = 5.8 TB/s, 0.89 of
+// the copy rate; of 8 K/V heads 34 us, 5 of them the merge; 11 fp32 rows over 2 x 32,760
+// tokens of 12 heads of 64 41 us, bound by issue slots (16 rows and two fp16 parts make about
+// 780 instructions per slab).
 #include <math.h>
 
 #include <algorithm>
