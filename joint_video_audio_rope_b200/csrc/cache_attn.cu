@@ -549,26 +549,37 @@ __global__ void __launch_bounds__(256)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
   const long long p0 = (long long)item * A.splits * tile + row;
-  float M = -INFINITY;
+  float M = -INFINITY, L = 0.f, out[W] = {};
+  constexpr int kBatch = 8;  // ranges whose sums are under way at once, beside the maxima
   for (int s = lane; s < A.splits; s += 32)
     M = fmaxf(M, A.part_ml[2 * (p0 + (long long)s * tile)]);
+  for (int s0 = warp % WPR; s0 < A.splits; s0 += WPR * kBatch) {
+    float2 ml[kBatch], x[kBatch][W / 2];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float Mr = M == -INFINITY ? 0.f : M;
-  float L = 0.f, out[W] = {};
-#pragma unroll 8
-  for (int s = warp % WPR; s < A.splits; s += WPR) {
-    const long long pr = p0 + (long long)s * tile;
-    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + 2 * pr);
-    // an empty range's sums are zeros: it adds nothing
-    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_approx(ml.x - Mr);
-    L = fmaf(f, ml.y, L);
-    const float* src = A.part_o + pr * D + lane * W;
+    for (int u = 0; u < kBatch; ++u) {
+      const long long pr = p0 + (long long)min(s0 + u * WPR, A.splits - 1) * tile;
+      ml[u] = *reinterpret_cast<const float2*>(A.part_ml + 2 * pr);
 #pragma unroll
-    for (int c = 0; c < W; c += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(src + c);
-      out[c] = fmaf(f, x.x, out[c]);
-      out[c + 1] = fmaf(f, x.y, out[c + 1]);
+      for (int c = 0; c < W / 2; ++c)
+        x[u][c] = *reinterpret_cast<const float2*>(A.part_o + pr * D + lane * W + 2 * c);
+    }
+    if (s0 < WPR) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    }
+    const float Mr = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      // an empty range's sums are zeros: it adds nothing
+      const bool none = s0 + u * WPR >= A.splits || (ml[u].x == -INFINITY && ml[u].y == 0.f);
+      if (none) continue;
+      const float f = ex2_approx(ml[u].x - Mr);
+      L = fmaf(f, ml[u].y, L);
+#pragma unroll
+      for (int c = 0; c < W / 2; ++c) {
+        out[2 * c] = fmaf(f, x[u][c].x, out[2 * c]);
+        out[2 * c + 1] = fmaf(f, x[u][c].y, out[2 * c + 1]);
+      }
     }
   }
   if constexpr (WPR > 1) {

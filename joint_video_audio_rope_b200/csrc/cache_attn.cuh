@@ -65,7 +65,6 @@ __device__ __forceinline__ int page_of(const CacheAttnArgs& A, int b, int n) {
   return (id >= 0 && id < A.n_pages) ? id : -1;
 }
 
-
 // What one CTA works on.
 struct CacheItem {
   int b, hk, r0, live;  // rows r0 .. r0 + live - 1

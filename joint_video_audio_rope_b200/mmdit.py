@@ -458,13 +458,19 @@ def _here(*tensors) -> list:
 _I32, _FLOAT = range(2)
 
 
+def _dtypes() -> tuple:
+    global _dtypes
+    import torch
+    kinds = (torch.int32, torch.float32)
+    _dtypes = lambda: kinds  # noqa: E731
+    return kinds
+
+
 def _array(x, kind: int, n: int, what: str) -> None:
     """Checks a packed per-item (or per-row) array of int32 or float32 (_I32, _FLOAT); ints and None pass."""
     if x is None or isinstance(x, int):
         return
-    import torch
-    if x.dtype is not (torch.int32 if kind == _I32 else torch.float32) or x.numel() != n or \
-            not x.is_contiguous():
+    if x.dtype is not _dtypes()[kind] or x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{what}: expected {n} packed values of {'int32' if kind == _I32 else 'float32'}")
 
 
