@@ -366,6 +366,10 @@ ATTN = [  # dtype, D, page, B, N, H, Hk, per, kv_len, q_len, causal
     ("bf16", 64, 128, 2, 90, 9, 3, 4, [512, 100], [90, 90], 1),
     ("bf16", 128, 16, 1, 200, 2, 2, 80, [1279], None, 0),
     ("bf16", 128, 128, 1, 66, 2, 2, 40, [5000], None, 0),
+    ("bf16", 64, 64, 2, 9, 2, 2, 10, [600, 9], None, 1),
+    ("bf16", 128, 64, 2, 27, 1, 1, 9, [576, 40], [27, 20], 1),
+    ("f32", 64, 32, 1, 2, 4, 2, 30, [900], None, 0),
+    ("f32", 128, 16, 2, 5, 2, 2, 20, [300, 7], [5, 2], 3),
     ("bf16", 64, 32, 200, 65, 2, 2, 90, [2880] + [40, 1, 129] * 66 + [2800], None, 1),  # more items than SMs: not split
 ]
 
