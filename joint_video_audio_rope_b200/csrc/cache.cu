@@ -2,21 +2,20 @@
 // copying pages (mmdit_cache_copy_pages).  Attention over it: cache_attn.cu.
 //
 // Append.  One CTA takes one page of one item and a slice of the heads, and
-// finds the page's angles once, into shared memory.  Per head it holds the new rows
-// of K and V in registers (NV 16-byte vectors of each per thread, so that a few
-// CTAs per SM keep enough loads in flight), finds max |x| of both with one
-// block reduction, and writes codes and scales: each value is read once (2 or
-// 4 bytes) and written once (1 byte), so the call is HBM bound.  A scale is a
-// power of two: e4m3 has its own exponent, so a finer scale would buy no precision,
-// and dividing by it, or moving a page to a larger one, rounds nothing but the code
-// itself.
+// finds the page's angles once, into shared memory.  The raw rows of K and V of the next
+// head are copied into a two-stage ring (cp.async; the first head's while the angles are
+// found) while the current head's maxima are found with one block reduction and its
+// codes and scales written: each value is read once (2 or 4 bytes) and written once (1
+// byte), so the call is HBM bound.  A scale is a power of two: e4m3 has its own
+// exponent, so a finer scale would buy no precision, and dividing by it, or moving a page
+// to a larger one, rounds nothing but the code itself.
 //
 // Copy.  The page lists travel in the kernel's parameters: no list has to be
 // copied to the device first, and one launch moves up to kCopyPairs pages.
 //
-// One B200: 32,760 tokens x 24 heads of 128 in bf16 (604 MB, floor 92 us) 105 us as they are,
-// 134 us with interleaved rotation, 200 us with half pairs (whose partners meet no
-// alignment and go through shared memory); 400 pages (315 MB, floor 48 us) 52 us.
+// One B200: 32,760 tokens x 24 heads of 128 in bf16 (604 MB, floor 92 us) 104 us as they are,
+// 122 us with interleaved rotation, 190 us with half pairs (whose partners meet no
+// alignment and cost single reads and writes of shared memory, and issue slots); 400 pages (315 MB, floor 48 us) 52 us.
 #include <cuda_fp16.h>
 #include <limits.h>
 
@@ -86,7 +85,7 @@ namespace {
 struct AppendArgs {
   const void *k, *v;
   long long st, sb;
-  int N, slice, cluster, mode;  // mode: 0 K as it is, 1 interleaved pairs, 2 half pairs
+  int N, slice, cluster, stages, mode;  // mode: 0 K as it is, 1 interleaved pairs, 2 half pairs
   const int32_t *start, *count;
   mmdit_cache c;
   int* err;
@@ -233,15 +232,20 @@ __device__ __forceinline__ void store_cluster(uint32_t to, int rank, float2 x) {
       : "memory");
 }
 
-// MODE: 0 K as it is, 1 interleaved pairs, 2 half pairs.  page * D / (NV 16-byte
-// vectors) threads.
-// MAXT: most threads; three CTAs of 256 per SM (up to 80 registers), or two with
-// eight vectors, keep 96 to 128 KB in flight.
-template <typename T, int MODE, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) append_kernel(const __grid_constant__ AppendArgs A) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// MODE: 0 K as it is, 1 interleaved pairs, 2 half pairs.  A thread has NV 16-byte vectors
+// of K and of V of each head: vectors tid + i threads of the page's rows.
+template <typename T, int MODE, int NV>
+__global__ void __launch_bounds__(512, NV == 2 ? 2 : 1)
+    append_kernel(const __grid_constant__ AppendArgs A) {
   constexpr int E = 16 / sizeof(T), P = E / 2;
-  // angles [page][D / 2] (cos, sin), then for half pairs: K rows in 32 bits
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int NP = NV * P;  // half pairs: pairs per thread
+  // the raw rows of K and V of `stages` heads; angles [page][D / 2] (cos, sin); half pairs:
+  // K's codes
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint2 red[2][16];  // by head parity: maxima of V and K per warp
   __shared__ uint32_t lost[4];  // rows with an infinity or NaN in K or V
   __shared__ double place[MODE == 0 ? 1 : 128][3];  // positions of the page's new rows
@@ -263,30 +267,44 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 
   const int cpr = D / E;  // vectors per row
   const int chunk = tid % cpr, row0 = tid / cpr, rstep = threads / cpr;
-  float2* angles = reinterpret_cast<float2*>(smem);
-  float* tile = reinterpret_cast<float*>(smem + (size_t)page * D * 4);
-  const int m2 = tid % (D / 2), prow0 = tid / (D / 2), pstep = threads / (D / 2);
+  const int half = page * D * (int)sizeof(T);  // bytes of K's (or V's) rows of a head
+  float2* angles = reinterpret_cast<float2*>(smem + (size_t)A.stages * 2 * half);
+  uint8_t* tile = reinterpret_cast<uint8_t*>(angles) + (size_t)page * D * 4;
+
+  const int h0 = blockIdx.y * A.slice, h1 = min(C.heads, h0 + A.slice);
+  const long long from0 = b * A.sb + (tok0 + row0) * A.st + chunk * E, step = rstep * A.st;
+  const uint32_t ring = smem_u32(smem) + tid * 16;
+  // copies a head's new rows into its stage; each thread reads its own vectors again
+  auto load = [&](int h) {
+    const T *kp = (const T*)A.k + from0 + (long long)h * D, *vp = (const T*)A.v + from0 + (long long)h * D;
+    const uint32_t to = ring + (A.stages == 2 ? (h - h0) & 1 : 0) * 2 * half;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int row = row0 + i * rstep;
+      if (row >= r_lo && row < r_hi) {
+        cp_async16(to + i * threads * 16, kp + i * step);
+        cp_async16(to + half + i * threads * 16, vp + i * step);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (h0 < h1) load(h0);  // under way while the angles are found
+
   // Interleaved bf16 pairs: a thread reads four angles as two 16-byte vectors.  The first
   // vectors of a row's chunks come first, then the second ones, so that
   // neighbouring threads read neighbouring vectors (no bank conflicts).
+  const int m2 = tid % (D / 2), prow0 = tid / (D / 2), pstep = threads / (D / 2);
   const int angle_at =
       MODE == 1 && P == 4 ? (m2 & 1) | (m2 >> 2) << 1 | ((m2 >> 1) & 1) * (D / 4) : m2;
-  // Half pairs: vectors of four channels of K; every second group of eight vectors swaps
-  // its neighbours, for the same reason.
-  auto swap = [](int ch) { return ch ^ ((ch >> 3) & 4); };
   int ch1 = 0, ch2 = 0;
-  if constexpr (MODE == 2) {
-    rotary_channels(A.tab, m2, ch1, ch2);
-    ch1 = swap(ch1);
-    ch2 = swap(ch2);
-  }
+  if constexpr (MODE == 2) rotary_channels(A.tab, m2, ch1, ch2);
   if constexpr (MODE != 0) {
     // The CTAs of a cluster share the page: each finds its part of the angles and
     // writes it to all of them.
     cluster_arrive();
-    if (tid < r_hi - r_lo) {
-      double* at = place[r_lo + tid];
-      token_position_f64(A.layout, p * page + r_lo + tid, at[0], at[1], at[2]);
+    for (int r = tid; r < r_hi - r_lo; r += threads) {
+      double* at = place[r_lo + r];
+      token_position_f64(A.layout, p * page + r_lo + r, at[0], at[1], at[2]);
     }
     __syncthreads();
     const int size = A.cluster, rank = blockIdx.y % size;
@@ -306,229 +324,219 @@ __global__ void __launch_bounds__(MAXT, MAXT == 512 ? 1 : NV == 8 ? 2 : 3) appen
 
   // the page's id is first needed here: its load ran under the work on the angles
   MMDIT_DCHECK(id >= 0 && id < C.n_pages, A.err);
-  if (id < 0 || id >= C.n_pages) return;
+  if (id < 0 || id >= C.n_pages) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
 
   constexpr uint32_t kInf = 0x7f800000u;
-  const int h0 = blockIdx.y * A.slice, h1 = min(C.heads, h0 + A.slice);
   // WHOLE: every row of the page is new, which spares the rows' checks.
   auto store_heads = [&](auto whole) {
-  constexpr bool WHOLE = decltype(whole)::value;
-  auto live = [&](int row) { return WHOLE || (row >= r_lo && row < r_hi); };
-  for (int h = h0; h < h1; ++h) {
-    const int par = (h - h0) & 1;
-    const long long from = b * A.sb + (tok0 + row0) * A.st + (long long)h * D + chunk * E;
-    const long long step = rstep * A.st;
-    const T *kp = (const T*)A.k + from, *vp = (const T*)A.v + from;
-    uint4 kr[NV], vr[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!WHOLE) kr[i] = vr[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (live(row0 + i * rstep)) {
-        kr[i] = __ldcs(reinterpret_cast<const uint4*>(kp + i * step));
-        vr[i] = __ldcs(reinterpret_cast<const uint4*>(vp + i * step));
+    constexpr bool WHOLE = decltype(whole)::value;
+    auto live = [&](int row) { return WHOLE || (row >= r_lo && row < r_hi); };
+    for (int h = h0; h < h1; ++h) {
+      const int par = (h - h0) & 1;
+      if (A.stages == 2 && h + 1 < h1) {
+        load(h + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-    }
-    const long long ph = (long long)id * C.heads + h;
-    uint8_t* kc = (uint8_t*)C.k + ph * page * D;
-    uint8_t* vc = (uint8_t*)C.v + ph * page * D;
-    float old_k = 0.f, old_v = 0.f;
-    if (!WHOLE && r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
+      const uint8_t* raw = smem + (A.stages == 2 ? par : 0) * 2 * half;
+      auto k_vec = [&](int i) { return *reinterpret_cast<const uint4*>(raw + (tid + i * threads) * 16); };
+      auto v_vec = [&](int i) {
+        return *reinterpret_cast<const uint4*>(raw + half + (tid + i * threads) * 16);
+      };
+      const long long ph = (long long)id * C.heads + h;
+      uint8_t* kc = (uint8_t*)C.k + ph * page * D;
+      uint8_t* vc = (uint8_t*)C.v + ph * page * D;
+      float old_k = 0.f, old_v = 0.f;
+      if (!WHOLE && r_lo > 0) old_k = C.k_scale[ph], old_v = C.v_scale[ph];
 
-    // ---- K turned: interleaved pairs in kx, half pairs in the tile; the largest |x|
-    [[maybe_unused]] float kx[MODE == 1 ? NV * E : 1];
-    uint32_t mv = 0u, mk = 0u;
-    if constexpr (MODE == 2) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float x[E];
-        values_of(kr[i], x, (T*)nullptr);
-        float* to = tile + (row0 + i * rstep) * D;
-#pragma unroll
-        for (int j = 0; j < E; j += 4)
-          *reinterpret_cast<float4*>(to + swap(chunk * E + j)) =
-              make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-      }
-      __syncthreads();
-      // four rows at a time: all loads, then all stores, which the compiler may not
-      // move past one another
-      for (int row = r_lo + prow0; row < r_hi; row += 4 * pstep) {
-        float x1[4], x2[4];
-        float2 cs[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = min(row + u * pstep, r_hi - 1);
-          x1[u] = tile[r * D + ch1];
-          x2[u] = tile[r * D + ch2];
-          cs[u] = angles[r * (D / 2) + m2];
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = row + u * pstep;
-          if (r >= r_hi) break;
-          const float t1 = x1[u] * cs[u].x - x2[u] * cs[u].y;
-          const float t2 = x1[u] * cs[u].y + x2[u] * cs[u].x;
-          tile[r * D + ch1] = t1;
-          tile[r * D + ch2] = t2;
-          mk = abs_bits(t1, t2, mk);
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      mv = vector_max(vr[i], mv, (T*)nullptr);
-      if constexpr (MODE == 0) mk = vector_max(kr[i], mk, (T*)nullptr);
-      if constexpr (MODE == 1) {
-        float x[E];
-        values_of(kr[i], x, (T*)nullptr);
-        const int row = row0 + i * rstep;
-        // rows without a new token hold zeros; their angles are not there
-        const float4* a = reinterpret_cast<const float4*>(
-            angles + (WHOLE ? row : min(max(row, r_lo), r_hi - 1)) * (D / 2)) + chunk;
-        float4 two;
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          if (j % 2 == 0) two = a[j / 2 * (D / 8)];
-          const float2 cs = j % 2 ? make_float2(two.z, two.w) : make_float2(two.x, two.y);
-          const float t1 = x[2 * j] * cs.x - x[2 * j + 1] * cs.y;
-          const float t2 = x[2 * j] * cs.y + x[2 * j + 1] * cs.x;
-          kx[i * E + 2 * j] = t1;
-          kx[i * E + 2 * j + 1] = t2;
-          mk = abs_bits(t1, t2, mk);
-        }
-      }
-    }
-    auto turned = [&](int i, float (&x)[E]) {  // vector i of K
-      if constexpr (MODE == 0) values_of(kr[i], x, (T*)nullptr);
-      if constexpr (MODE == 1) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) x[j] = kx[i * E + j];
-      }
+      // ---- K turned, and the largest |x|
+      [[maybe_unused]] float kx[MODE == 0 ? 1 : NV * E];
+      uint32_t mv = 0u, mk = 0u;
       if constexpr (MODE == 2) {
-        const float* t = tile + (row0 + i * rstep) * D;
+        __syncthreads();  // the rows that other threads copied
+        const T* rows = reinterpret_cast<const T*>(raw);
 #pragma unroll
-        for (int j = 0; j < E; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(t + swap(chunk * E + j));
-          x[j] = f.x, x[j + 1] = f.y, x[j + 2] = f.z, x[j + 3] = f.w;
+        for (int i = 0; i < NP; ++i) {
+          const int row = prow0 + i * pstep;
+          kx[2 * i] = kx[2 * i + 1] = 0.f;
+          if (!live(row)) continue;
+          const float x1 = (float)rows[row * D + ch1], x2 = (float)rows[row * D + ch2];
+          const float2 cs = angles[row * (D / 2) + m2];
+          kx[2 * i] = x1 * cs.x - x2 * cs.y;
+          kx[2 * i + 1] = x1 * cs.y + x2 * cs.x;
+          mk = abs_bits(kx[2 * i], kx[2 * i + 1], mk);
         }
       }
-    };
-    auto block_max = [&](uint2* r) {
-      mv = __reduce_max_sync(0xffffffffu, mv);
-      mk = __reduce_max_sync(0xffffffffu, mk);
-      if ((tid & 31) == 0) r[tid >> 5] = make_uint2(mv, mk);
-      __syncthreads();
-      for (int i = 0; i < warps; ++i) {
-        const uint2 m = r[i];
-        mv = max(mv, m.x);
-        mk = max(mk, m.y);
-      }
-    };
-    block_max(red[par]);
-    const bool careful = max(mv, mk) >= kInf;  // the same in every thread
-    if (careful) {
-      // an infinity or NaN: mark its rows, leave it out of V and of the maxima
-      __syncthreads();
-      if (tid < 4) lost[tid] = 0u;
-      __syncthreads();
-      mv = mk = 0u;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * rstep;
         if (!live(row)) continue;
-        bool ok = keep_numbers(vr[i], (T*)nullptr);
-        mv = vector_max(vr[i], mv, (T*)nullptr);
-        uint4 raw = *reinterpret_cast<const uint4*>(kp + i * step);
-        ok = keep_numbers(raw, (T*)nullptr) && ok;
-        if (!ok) atomicOr(&lost[row >> 5], 1u << (row & 31));
-        float x[E];
-        turned(i, x);
+        mv = vector_max(v_vec(i), mv, (T*)nullptr);
+        if constexpr (MODE == 0) mk = vector_max(k_vec(i), mk, (T*)nullptr);
+        if constexpr (MODE == 1) {
+          float x[E];
+          values_of(k_vec(i), x, (T*)nullptr);
+          const float4* a = reinterpret_cast<const float4*>(angles + row * (D / 2)) + chunk;
+          float4 two;
 #pragma unroll
-        for (int j = 0; j < E; ++j)
-          if (is_number(x[j])) mk = abs_bits(x[j], 0.f, mk);
+          for (int j = 0; j < P; ++j) {
+            if (j % 2 == 0) two = a[j / 2 * (D / 8)];
+            const float2 cs = j % 2 ? make_float2(two.z, two.w) : make_float2(two.x, two.y);
+            const float t1 = x[2 * j] * cs.x - x[2 * j + 1] * cs.y;
+            const float t2 = x[2 * j] * cs.y + x[2 * j + 1] * cs.x;
+            kx[i * E + 2 * j] = t1;
+            kx[i * E + 2 * j + 1] = t2;
+            mk = abs_bits(t1, t2, mk);
+          }
+        }
       }
+      auto block_max = [&](uint2* r) {
+        mv = __reduce_max_sync(0xffffffffu, mv);
+        mk = __reduce_max_sync(0xffffffffu, mk);
+        if ((tid & 31) == 0) r[tid >> 5] = make_uint2(mv, mk);
+        __syncthreads();
+        for (int i = 0; i < warps; ++i) {
+          const uint2 m = r[i];
+          mv = max(mv, m.x);
+          mk = max(mk, m.y);
+        }
+      };
       block_max(red[par]);
-    }
+      const bool careful = max(mv, mk) >= kInf;  // the same in every thread
+      if (careful) {
+        // an infinity or NaN: mark its rows, leave it out of V and of the maxima
+        __syncthreads();
+        if (tid < 4) lost[tid] = 0u;
+        __syncthreads();
+        mv = mk = 0u;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int row = row0 + i * rstep;
+          if (!live(row)) continue;
+          uint4 v = v_vec(i), k = k_vec(i);
+          bool ok = keep_numbers(v, (T*)nullptr);
+          mv = vector_max(v, mv, (T*)nullptr);
+          ok = keep_numbers(k, (T*)nullptr) && ok;
+          if constexpr (MODE == 0) mk = vector_max(k, mk, (T*)nullptr);
+          if (!ok) atomicOr(&lost[row >> 5], 1u << (row & 31));
+        }
+        if constexpr (MODE != 0) {
+#pragma unroll
+          for (int j = 0; j < NV * E; ++j)
+            if (WHOLE || MODE == 2 || live(row0 + j / E * rstep))
+              if (is_number(kx[j])) mk = abs_bits(kx[j], 0.f, mk);
+        }
+        block_max(red[par]);
+      }
 
-    // ---- scales; every thread has read the old ones before that barrier
-    float sv = fit_scale(__uint_as_float(mv)), sk = fit_scale(__uint_as_float(mk));
-    if (!WHOLE && r_lo > 0) {
-      sv = fmaxf(sv, floor_scale(old_v));
-      sk = fmaxf(sk, floor_scale(old_k));
-      if (sv > old_v) rescale_codes(vc, r_lo * D, old_v / sv, tid, threads);
-      if (sk > old_k) rescale_codes(kc, r_lo * D, old_k / sk, tid, threads);
-    }
-    if (tid == 0) {
-      C.v_scale[ph] = sv;
-      C.k_scale[ph] = sk;
-    }
-    const float iv = inverse_pow2(sv), ik = inverse_pow2(sk);
+      // ---- scales; every thread has read the old ones before that barrier
+      float sv = fit_scale(__uint_as_float(mv)), sk = fit_scale(__uint_as_float(mk));
+      if (!WHOLE && r_lo > 0) {
+        sv = fmaxf(sv, floor_scale(old_v));
+        sk = fmaxf(sk, floor_scale(old_k));
+        if (sv > old_v) rescale_codes(vc, r_lo * D, old_v / sv, tid, threads);
+        if (sk > old_k) rescale_codes(kc, r_lo * D, old_k / sk, tid, threads);
+      }
+      if (tid == 0) {
+        C.v_scale[ph] = sv;
+        C.k_scale[ph] = sk;
+      }
+      const float iv = inverse_pow2(sv), ik = inverse_pow2(sk);
 
-    // ---- codes
+      // ---- codes
+      if constexpr (MODE == 2) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int row = row0 + i * rstep;
-      if (!live(row)) continue;
-      const int to = row * D + chunk * E;
-      uint32_t w[E / 4], v[E / 4];
-      float x[E];
-      scaled_values(vr[i], iv, x, (T*)nullptr);
-#pragma unroll
-      for (int j = 0; j < E / 4; ++j)
-        v[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      if constexpr (MODE == 0) {
-        scaled_values(kr[i], ik, x, (T*)nullptr);
-      } else {
-        turned(i, x);
-#pragma unroll
-        for (int j = 0; j < E; ++j) x[j] *= ik;
+        for (int i = 0; i < NP; ++i) {
+          const int row = prow0 + i * pstep;
+          const uint32_t two = codes4(kx[2 * i] * ik, kx[2 * i + 1] * ik, 0.f, 0.f);
+          tile[row * D + ch1] = (uint8_t)two;
+          tile[row * D + ch2] = (uint8_t)(two >> 8);
+        }
+        __syncthreads();
       }
 #pragma unroll
-      for (int j = 0; j < E / 4; ++j)
-        w[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-      if (careful && ((lost[row >> 5] >> (row & 31)) & 1u)) {
+      for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * rstep;
+        if (!live(row)) continue;
+        const int to = row * D + chunk * E;
+        uint32_t w[E / 4], v[E / 4];
+        float x[E];
+        uint4 r = v_vec(i);
+        if (careful) keep_numbers(r, (T*)nullptr);
+        scaled_values(r, iv, x, (T*)nullptr);
 #pragma unroll
-        for (int j = 0; j < E / 4; ++j) w[j] = 0x7f7f7f7fu;
+        for (int j = 0; j < E / 4; ++j)
+          v[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        if constexpr (MODE == 2) {
+#pragma unroll
+          for (int j = 0; j < E / 4; ++j) w[j] = *reinterpret_cast<const uint32_t*>(tile + to + 4 * j);
+        } else {
+          if constexpr (MODE == 0) {
+            scaled_values(k_vec(i), ik, x, (T*)nullptr);
+          } else {
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[j] = kx[i * E + j] * ik;
+          }
+#pragma unroll
+          for (int j = 0; j < E / 4; ++j)
+            w[j] = codes4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        }
+        if (careful && ((lost[row >> 5] >> (row & 31)) & 1u)) {
+#pragma unroll
+          for (int j = 0; j < E / 4; ++j) w[j] = 0x7f7f7f7fu;
+        }
+        if constexpr (E == 8) {
+          *reinterpret_cast<uint2*>(vc + to) = make_uint2(v[0], v[1]);
+          *reinterpret_cast<uint2*>(kc + to) = make_uint2(w[0], w[1]);
+        } else {
+          *reinterpret_cast<uint32_t*>(vc + to) = v[0];
+          *reinterpret_cast<uint32_t*>(kc + to) = w[0];
+        }
       }
-      if constexpr (E == 8) {
-        *reinterpret_cast<uint2*>(vc + to) = make_uint2(v[0], v[1]);
-        *reinterpret_cast<uint2*>(kc + to) = make_uint2(w[0], w[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(vc + to) = v[0];
-        *reinterpret_cast<uint32_t*>(kc + to) = w[0];
+      if (A.stages == 1 && h + 1 < h1) {
+        if (MODE == 2) __syncthreads();  // every thread is done with the rows
+        load(h + 1);
       }
     }
-  }
   };
   if (r_lo == 0 && r_hi == page) store_heads(std::true_type{});
   else store_heads(std::false_type{});
 }
 
-template <typename T, int MODE, int NV, int MAXT>
+template <typename T, int MODE, int NV>
 cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
   const int page = A.c.page_tokens, D = A.c.head_dim;
-  const int threads = page * D * (int)sizeof(T) / (16 * NV);
-  const int smem = page * D * 4 * MODE;  // angles, K rows
+  const int rows = 2 * page * D * (int)sizeof(T);  // K's and V's rows of a head
+  const int threads = rows / (32 * NV);
+  const int rest = (MODE == 0 ? 0 : page * D * 4) + (MODE == 2 ? page * D : 0);
+  constexpr int kMost = 227 * 1024 - 4096;  // static shared memory and the launch's own
+  A.stages = 2 * rows + rest <= kMost ? 2 : 1;
+  const int smem = A.stages * rows + rest;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once_per_device(dev, [] {
-    return cudaFuncSetAttribute(append_kernel<T, MODE, NV, MAXT>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                128 * 128 * 4 * MODE);
+    return cudaFuncSetAttribute(append_kernel<T, MODE, NV>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (e != cudaSuccess) return e;
   const int pages = (int)((A.N + page - 2LL) / page) + 1;  // most pages that N tokens touch
   // Slices of the heads, one CTA each: a CTA takes as long as its heads and about two
-  // more for the page's look-ups and angles, and about 768 threads fit an SM; the number of
-  // slices with the shortest waves is taken (480p clip, bf16, interleaved: 136 us with 4
-  // slices, 157 with 2, 160 with 12).  Where K is turned, the CTAs of a page form clusters of
-  // up to eight that share the work on its angles (the same with clusters of 1: 200 us).
-  const long long resident = 148LL * std::max(1, 768 / threads);
+  // more for the page's look-ups and angles, and there are as many waves as the CTAs are of
+  // what fits (480p clip, bf16, interleaved: 122 us with one or two slices, 126 with four, 160 with
+  // eight; 1,560 tokens of it: 38, 23, 15 and 13).  Where K is turned, the CTAs of a page form
+  // clusters of up to eight that share the work on its angles.
+  const long long resident =
+      148LL * std::max(1, std::min((NV == 2 ? 1024 : 512) / threads, 227 * 1024 / (smem + 4096)));
   int slices = 1, size = 1;
   long long best = 0;
   for (int n = 1; n <= std::min(A.c.heads, 256); n += n < 8 ? n : 8) {
-    const long long waves = ((long long)pages * batch * n + resident - 1) / resident;
-    const long long cost = waves * ((A.c.heads + n - 1) / n + 2);
+    const long long cost = std::max(resident, (long long)pages * batch * n) *
+                           ((A.c.heads + n - 1) / n + 2);
     if (n == 1 || cost < best) best = cost, slices = n;
   }
   A.slice = (A.c.heads + slices - 1) / slices;
@@ -549,25 +557,26 @@ cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   A.cluster = size;
-  return cudaLaunchKernelEx(&cfg, append_kernel<T, MODE, NV, MAXT>, A);
+  return cudaLaunchKernelEx(&cfg, append_kernel<T, MODE, NV>, A);
 }
 
-template <typename T, int NV, int MAXT>
+template <typename T, int NV>
 cudaError_t launch_append_pairs(AppendArgs& A, int batch, cudaStream_t s) {
-  if (A.mode == 0) return launch_append_mode<T, 0, NV, MAXT>(A, batch, s);
-  if (A.mode == 1) return launch_append_mode<T, 1, NV, MAXT>(A, batch, s);
-  return launch_append_mode<T, 2, NV, MAXT>(A, batch, s);
+  if (A.mode == 0) return launch_append_mode<T, 0, NV>(A, batch, s);
+  if (A.mode == 1) return launch_append_mode<T, 1, NV>(A, batch, s);
+  return launch_append_mode<T, 2, NV>(A, batch, s);
 }
 
 template <typename T>
 cudaError_t launch_append(AppendArgs& A, int batch, cudaStream_t s) {
-  // 4 vectors per thread, 8 where that would take more than 256 threads (one CTA of
-  // 512 fills an SM less than two of 256 with twice the loads each)
+  // Two vectors of K and of V per thread for pages up to 8 KB, four above (two CTAs of 256
+  // threads: 123 us for the 480p clip in pages of 64; 512 threads with two: 144), eight where that
+  // would take over 512 threads.
   const int vectors = A.c.page_tokens * A.c.head_dim * (int)sizeof(T) / 16;
-  if (vectors <= 1024) return launch_append_pairs<T, 4, 256>(A, batch, s);
+  if (vectors <= 512) return launch_append_pairs<T, 2>(A, batch, s);
   if constexpr (sizeof(T) == 4)
-    if (vectors > 2048) return launch_append_pairs<T, 8, 512>(A, batch, s);
-  return launch_append_pairs<T, 8, 256>(A, batch, s);
+    if (vectors > 2048) return launch_append_pairs<T, 8>(A, batch, s);
+  return launch_append_pairs<T, 4>(A, batch, s);
 }
 
 // Every copy of a call runs at once: a page written twice, or read and written,
