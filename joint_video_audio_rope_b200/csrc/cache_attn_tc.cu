@@ -20,9 +20,9 @@
 // of the largest are still held.  The sum of weights adds up 2^(t - m + 7) / (V scale) per
 // group.
 //
-// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.55 to 1.77 ms (1,330 to 1,160 TFLOP/s, the cache in L2
-// or not); 218 rows x 24 heads over 32,760 tokens 111 us.  A row tile's chain (scores out,
-// softmax, P in, product) is what bounds it: 1.9 us per 128 keys with two tiles in turn, the
+// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.58 ms at full clocks (1,304 TFLOP/s), 1.81 ms
+// under the power cap (1,138 TFLOP/s); 218 rows x 24 heads over 32,760 tokens 103 to 111 us. A row
+// tile's chain (scores out, softmax, P in, product) is what bounds it: 1.9 us per 128 keys with two tiles in turn, the
 // tensor pipe at 57 %, the exponentials at 58 % of their pipe, shared memory at 77 %.
 #include <math.h>
 
