@@ -74,11 +74,6 @@ __device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -221,8 +216,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     const int rr = 8 * q + g, r = r0 + rr;
-    const T* src = (const T*)A.q + b * A.q_sb + (long long)(r / A.G) * A.q_st +
-                   (long long)(hk * A.G + r % A.G) * D;
+    const int rt = row_token(A, r);
+    const T* src = (const T*)A.q + b * A.q_sb + (long long)rt * A.q_st +
+                   (long long)(hk * A.G + r - rt * A.G) * D;
     float x[KK][4], am = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
@@ -248,13 +244,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
           x1 -= y.y;
         }
       }
-    const float m = A.scale_log2 / f;
+    const float m = A.scale_log2 * inverse_pow2(f);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       mul[q][e] = __shfl_sync(0xffffffffu, m, (2 * t + e) * 4);
       // rows behind the last are computed with it and not stored
       const int row = min(8 * q + 2 * t + e, live - 1);
-      limit[q][e] = visible_keys(A, kv, ql, (r0 + row) / A.G);
+      limit[q][e] = visible_keys(A, kv, ql, row_token(A, r0 + row));
       full = min(full, limit[q][e]);
     }
   }
@@ -513,7 +509,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
     }
     return;
   }
-  const int tok = r / A.G, head = hk * A.G + r % A.G;
+  const int tok = row_token(A, r), head = hk * A.G + r - tok * A.G;
   const float inv = L == 0.f ? 0.f : 1.f / L;  // a NaN stays one
   T* dst = (T*)A.o + b * A.o_sb + (long long)tok * A.o_st + (long long)head * D;
 #pragma unroll
@@ -544,7 +540,7 @@ __global__ void __launch_bounds__(256)
   const int item = i / tile, row = i % tile;
   int b, hk, r0;
   item_rows(A, A.whole + item, tile, b, hk, r0);
-  const int r = r0 + row, tok = r / A.G, head = hk * A.G + r % A.G;
+  const int r = r0 + row, tok = row_token(A, r), head = hk * A.G + r - tok * A.G;
   const bool live = b < A.B && tok < query_tokens(A, b);  // the same in all warps of a row
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
@@ -779,6 +775,8 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   A.H = q_desc->heads;
   A.Hk = cache->heads;
   A.G = A.H / A.Hk;
+  while ((1LL << A.g_shift) < A.G) ++A.g_shift;
+  A.g_mul = (uint32_t)(((1ull << 32) * ((1ull << A.g_shift) - A.G)) / A.G + 1);
   A.causal = causal_block;
   A.scale_log2 = scale * 1.4426950408889634f;
   A.tiles = plan.tiles;

@@ -27,7 +27,9 @@ struct CacheAttnArgs {
   const float *k_scale, *v_scale;
   const int32_t *table, *kv_len, *q_len;
   int n_pages, page, page_log2, max_pages;
-  int B, N, H, Hk, G;  // G = H / Hk
+  int B, N, H, Hk, G;   // G = H / Hk
+  uint32_t g_mul;       // r / G = (mulhi(r, g_mul) + r) >> g_shift for r < 2^31
+  int g_shift;
   int causal;
   float scale_log2;
   // Items: one tile of rows of one (item, K/V head).  The first `whole` of them
@@ -57,6 +59,11 @@ __device__ __forceinline__ int visible_keys(const CacheAttnArgs& A, int kv, int 
   if (p < 0) return 0;
   const long long end = ((long long)(p / A.causal) + 1) * A.causal;
   return end < kv ? (int)end : kv;
+}
+// Token of row r; its query head is hk G + r - token G.  (A division costs as much as the
+// row's load; a tile has 256 rows to address.)
+__device__ __forceinline__ int row_token(const CacheAttnArgs& A, int r) {
+  return (int)((__umulhi((uint32_t)r, A.g_mul) + (uint32_t)r) >> A.g_shift);
 }
 // Page of token n of item b, or -1 (nothing to see there).
 __device__ __forceinline__ int page_of(const CacheAttnArgs& A, int b, int n) {
@@ -97,7 +104,7 @@ __device__ __forceinline__ CacheItem item_of(const CacheAttnArgs& A, int i, int 
   w.live = min(tile, w.ql * A.G - w.r0);
   w.lo = w.hi = 0;
   if (w.live > 0) {
-    const int keys = visible_keys(A, w.kv, w.ql, (w.r0 + w.live - 1) / A.G);
+    const int keys = visible_keys(A, w.kv, w.ql, row_token(A, w.r0 + w.live - 1));
     const int units = (keys + kUnit - 1) / kUnit, per = (units + splits - 1) / splits;
     w.lo = min(keys, split * per * kUnit);
     w.hi = min(keys, w.lo + per * kUnit);
@@ -111,6 +118,10 @@ __device__ __forceinline__ float fit_half(float amax) {
   const int e = (__float_as_int(amax) >> 23) - 127;  // amax < 2^(e+1)
   return __int_as_float((min(max(14 - e, -126), 126) + 127) << 23);
 }
+// 1 / f of a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_pow2(float f) {
+  return __int_as_float((254 << 23) - __float_as_int(f));
+}
 // Four e4m3 codes as two pairs of fp16 (as one 32-bit register each: through the 16-bit
 // halves of the type's C++ interface this took three times the operations).
 __device__ __forceinline__ void halves_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
@@ -123,6 +134,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// 16 bytes to shared memory, asynchronously; zeros if not there.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
 
 // bf16 q; `grid` CTAs (cache_attn_tc.cu)

@@ -353,41 +353,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (t < nt) {
       if (tiles > 0) {
         // Q rows of this warp: fp16, largest value at 2^14..2^15
+        // Copied to their places as they are, all at once, then turned into fp16 there by
+        // the lane that copied them.  Short loops: code that runs once costs its fetch.
         constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per step
-        const int c = lane % LPR;
-        uint4 rows[32 / RPI];  // all loads at once
-#pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int n = warp * 32 + i * RPI + lane / LPR, r = w.r0 + n;
-          rows[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (n < w.live)
-            rows[i] = *reinterpret_cast<const uint4*>(
-                (const __nv_bfloat16*)A.q + w.b * A.q_sb + (long long)(r / A.G) * A.q_st +
-                (long long)(w.hk * A.G + r % A.G) * D + c * 8);
+        const int c = lane % LPR, first = warp * 32 + lane / LPR;
+        uint8_t* place = smem + t * C::kTile + (c >> 3) * kHalf;
+        auto at = [&](int n) { return place + (n & 127) * 128 + (((c & 7) ^ (n & 7)) << 4); };
+#pragma unroll 2
+        for (int i = 0; i < 32; i += RPI) {
+          const int n = first + i, r = w.r0 + n, tok = row_token(A, r);
+          const bool there = n < w.live;
+          const __nv_bfloat16* src = (const __nv_bfloat16*)A.q;
+          if (there)
+            src += w.b * A.q_sb + (long long)tok * A.q_st +
+                   (long long)(w.hk * A.G + r - tok * A.G) * D + c * 8;
+          cp_async16_if(smem_u32(at(n)), src, there);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        constexpr int U = 4;  // rows whose maxima are found side by side
+#pragma unroll 1
+        for (int i = 0; i < 32; i += U * RPI) {
+          uint4 v[U];
+          float am[U];
 #pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
-          const int n = warp * 32 + i * RPI + lane / LPR;
-          uint4 v = rows[i];
-          const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v);
-          float2 x[4];
-          float am = 0.f;
+          for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const uint4*>(at(first + i + u * RPI));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = __bfloat1622float2(p[k]);
-            am = fmaxf(am, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+          for (int u = 0; u < U; ++u) {
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
+            am[u] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = __bfloat1622float2(p[k]);
+              am[u] = max3f(am[u], fabsf(x.x), fabsf(x.y));
+            }
           }
 #pragma unroll
           for (int off = LPR / 2; off > 0; off >>= 1)
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
-          const float f = fit_half(am);
-          v.x = pack_half2(x[0].x * f, x[0].y * f);
-          v.y = pack_half2(x[1].x * f, x[1].y * f);
-          v.z = pack_half2(x[2].x * f, x[2].y * f);
-          v.w = pack_half2(x[3].x * f, x[3].y * f);
-          *reinterpret_cast<uint4*>(smem + t * C::kTile + (c >> 3) * kHalf + (n & 127) * 128 +
-                                    (((c & 7) ^ (n & 7)) << 4)) = v;
-          if (c == 0) muls[n] = A.scale_log2 / f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              am[u] = fmaxf(am[u], __shfl_xor_sync(0xffffffffu, am[u], off));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int n = first + i + u * RPI;
+            const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&v[u]);
+            const float f = fit_half(am[u]);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = __bfloat1622float2(p[k]);
+              h[k] = pack_half2(x.x * f, x.y * f);
+            }
+            *reinterpret_cast<uint4*>(at(n)) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (c == 0) muls[n] = A.scale_log2 * inverse_pow2(f);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(M_QREADY + t));
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float mul = muls[row];
       // rows behind the last are computed with it and not stored
-      const int limit = visible_keys(A, w.kv, w.ql, (w.r0 + min(row, w.live - 1)) / A.G);
+      const int limit = visible_keys(A, w.kv, w.ql, row_token(A, w.r0 + min(row, w.live - 1)));
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t s_addr = tmem + lane_off + t * 128;
       const uint32_t o_addr = tmem + lane_off + 256 + t * D;
@@ -508,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const float mref = m == -INFINITY ? -INFINITY : m - kManyShift;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
-        const int r = w.r0 + row, tok = r / A.G, head = w.hk * A.G + r % A.G;
+        const int r = w.r0 + row, tok = row_token(A, r), head = w.hk * A.G + r - tok * A.G;
         const long long pr = w.part * kManyTile + row;
         uint8_t* stage = smem + t * C::kTile + (warp & 3) * (32 * D * 2);  // Q's place
         constexpr int CH = D / 8;  // 16-byte chunks per output row
@@ -560,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; i += 32 / CH) {
             const int n = i + lane / CH, chunk = lane % CH, rr = warp * 32 + n;
             if (rr < w.live) {
-              const int q = w.r0 + rr;
+              const int q = w.r0 + rr, qt = row_token(A, q);
               *reinterpret_cast<uint4*>((__nv_bfloat16*)A.o + w.b * A.o_sb +
-                                        (long long)(q / A.G) * A.o_st +
-                                        (long long)(w.hk * A.G + q % A.G) * D + chunk * 8) =
+                                        (long long)qt * A.o_st +
+                                        (long long)(w.hk * A.G + q - qt * A.G) * D + chunk * 8) =
                   *reinterpret_cast<const uint4*>(stage + n * (D * 2) + ((chunk ^ (n & 7)) << 4));
             }
           }
