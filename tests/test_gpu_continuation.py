@@ -92,6 +92,9 @@ ROTARY = [  # dtype, D, B, N, Hq, Hk, dims, half, scaling, transpose, pads, wind
     ("f32", 128, 1, 7, 9, 3, (2, 0, 126), True, "parts", False, (0, 0), True),
     ("f32", 128, 2, 130, 1, 1, (10, 6, 0), False, "parts", True, (0, 0), True),
     ("f32", 64, 1, 291, 2, 1, (64, 0, 0), False, "ntk", False, (0, 0), False),
+    # enough tokens that a thread streams several heads past its angles
+    ("bf16", 64, 8, 1100, 9, 4, (24, 20, 20), True, "none", False, (8, 0), True),
+    ("f32", 64, 8, 600, 10, 3, (32, 16, 16), False, "parts", True, (0, 4), True),
 ]
 
 
@@ -101,7 +104,7 @@ def test_rotary(M, case):
     rng = np.random.default_rng(5)
     segs = _segments(M)
     mp, p = _params(M, dims, half, scaling)
-    first = np.array([40, 0, 280][:B] if window else [0] * B, np.int32)
+    first = np.resize([40, 0, 280] if window else [0], B).astype(np.int32)
     q, _ = _tensor(rng, (B, N, hq, D), dtype, pt, pb)
     k, _ = _tensor(rng, (B, N, hk, D), dtype, 2 * pt, pb)
     qo, qflat = _tensor(rng, (B, N, hq, D), dtype, pt + 16, 32, fill=np.zeros((B, N, hq, D)))
@@ -209,6 +212,12 @@ APPEND = [  # dtype, D, page, B, N, H, start, count, rotation (None or half)
     ("f32", 128, 32, 1, 40, 2, [5], None, False),
     ("f32", 128, 128, 1, 200, 2, [100], None, True),
     ("bf16", 64, 128, 2, 9, 2, [0, 120], None, False),
+    # so many items that a CTA takes several heads of its page, one or two of them in shared memory
+    ("f32", 128, 128, 80, 3, 4, [7 * i % 300 for i in range(80)], None, True),
+    ("f32", 128, 128, 80, 3, 5, [11 * i % 300 for i in range(80)], None, False),
+    ("bf16", 128, 64, 200, 2, 4, [3 * i % 130 for i in range(200)], [i % 3 for i in range(200)], True),
+    ("bf16", 64, 64, 200, 70, 3, [i % 70 for i in range(200)], None, None),
+    ("f32", 64, 16, 300, 2, 6, [i % 40 for i in range(300)], None, False),
 ]
 
 
@@ -302,6 +311,24 @@ def test_append_of_infinities_and_nan(M, dtype, half):
     if half is None:
         OC.append(host[0], host[2], host[4], hk, [0], [60], bad)
         assert np.array_equal(got, host[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_infinities_to_several_heads_of_a_cta(M, dtype):
+    """300 items of 5 heads: heads with and without an infinity or NaN follow one another in a CTA."""
+    rng = np.random.default_rng(15)
+    B, N, H = 300, 3, 5
+    host, dev, cache = _new_cache(M, rng, B + 2, H, 64, 64, B, 1)
+    x = [rng.standard_normal((B, N, H, 64)) for _ in range(2)]
+    for i, bad in enumerate((np.nan, np.inf, -np.inf)):
+        x[i % 2][i::7, i, i + 1, 5 * i] = bad
+    (k, _), (v, _) = (_tensor(rng, (B, N, H, 64), dtype, fill=a) for a in x)
+    bad = ~(np.isfinite(x[0]) & np.isfinite(x[1])).all(-1)
+    M.cache_append(k, v, M.desc_of(k), cache, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    OC.append(host[0], host[2], host[4], _f64(k), [0] * B, [N] * B, bad)
+    OC.append(host[1], host[3], host[4], _f64(v), [0] * B, [N] * B, None)
+    for d, h in zip(dev[:4], host):
+        assert np.array_equal(d.cpu().numpy(), h)
 
 
 def test_append_token_by_token_equals_its_definition(M):
