@@ -627,12 +627,12 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
   p.tiles = (int)((rows + p.tile - 1) / p.tile);
   p.items = (long long)p.tiles * c.heads * q.batch;
   if (p.tile != kManyTile) {
-    // A wave of three CTAs of four warps per SM (two where their registers fit no third); a
-    // range is at least 512 tokens (16 slabs for the CTA), or its merge costs more than it
-    // saves.
+    // A wave of as many CTAs as fit (Few::kCtas); a range is at least 256 tokens, two slabs per
+    // warp, and a history of up to 512 is not split (3 rows x 8 heads over 20,000 tokens: 14.4 us
+    // in ranges of 256, 16.1 of 512; over 1,000: 10.9 and 14.8).
     const int weight = q.head_dim * (p.tile / 8) * (q.dtype == MMDIT_F32 ? 2 : 1);
     p.splits = (int)std::max(
-        1LL, std::min((weight > 256 ? 2 : 3) * 148 / p.items, (cap + 511) / 512));
+        1LL, std::min((weight > 256 ? 2 : 3) * 148 / p.items, cap <= 512 ? 1 : (cap + 255) / 256));
     p.whole = p.splits > 1 ? 0 : p.items;
   } else {
     // One CTA per SM.  What is left behind the whole waves is split so that its
