@@ -539,7 +539,8 @@ typedef struct {
   void* k;                    /* codes, 16-byte aligned */
   void* v;
   float* k_scale;             /* device float [n_pages, heads], each 0 or in 2^-60..2^60 */
-  float* v_scale;             /* (V scales of one item and head within 2^80 of one another) */
+  float* v_scale;             /* (V scales of one item and head within 2^80 of one another,
+                                 and up to 2^30 beside a scale of 0) */
   int32_t n_pages;
   int32_t heads;              /* K/V heads */
   int32_t page_tokens;        /* 16, 32, 64 or 128 */

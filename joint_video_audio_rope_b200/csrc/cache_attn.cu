@@ -314,9 +314,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       const float4 m4 = meta[f];
       kf[f] = m4.x;
       // a page that is not there is not seen; a V scale of 0 stands for zeros
-      lv[f] = m4.z + (m4.y > 0.f ? log2_normal(m4.y) : 0.f);
+      lv[f] = m4.z + (m4.y > 0.f ? log2_normal(m4.y) : kNoScaleLog2);
       iv[f] = m4.y > 0.f ? __frcp_rn(m4.y) : 0.f;
-      wv[f] = m4.y > 0.f ? iv[f] : 1.f;
+      wv[f] = m4.y > 0.f ? iv[f] : kNoScaleInverse;
     }
 #pragma unroll
     for (int q = 0; q < NQ; ++q)

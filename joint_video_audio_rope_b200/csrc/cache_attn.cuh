@@ -8,8 +8,10 @@
 // Scales.  K's scale multiplies the scores.  V's scale is folded into the
 // exponent: with t = s log2(e) + log2(vs) and its running maximum m, the
 // kernels form p' = 2^(t - m) <= 1, accumulate p' x code, and the sum of
-// weights as p' / vs.  p' is fit for fp16 whatever the scales are, and the
-// result needs no pass over V's values.
+// weights as p' / vs.  So p' is measured against what the row's largest term adds to
+// the output, and the result needs no pass over V's values.  A V scale of 0 (zeros, whatever
+// the codes) is taken as the smallest one, 2^-60, over codes of zero: it counts in the
+// sum of weights and must not raise m, which would push the other terms out of fp16.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -45,6 +47,8 @@ struct CacheAttnArgs {
 // bf16 rows, on tcgen05: cache_attn_tc.cu).
 constexpr int kManyTile = 256;
 constexpr int kUnit = 128;      // tokens: granularity of the split key ranges
+constexpr float kNoScaleLog2 = -60.f;                  // of a V scale of 0
+constexpr float kNoScaleInverse = 1152921504606846976.f;  // 2^60
 
 __device__ __forceinline__ int held_tokens(const CacheAttnArgs& A, int b) {
   return min(max(A.kv_len[b], 0), A.max_pages * A.page);

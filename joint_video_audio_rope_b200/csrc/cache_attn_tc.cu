@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 13 && !skip) {
       // ---------------------------------------------------------- pages
       // Lane g < 8 looks up group g of every tile.  A page that is not there is not
-      // seen; a V scale of 0 (held as inverse -1) stands for zeros.
+      // seen; a V scale of 0 (its inverse held as a negative number) stands for zeros.
       bool ok = true;
       for (int j = 0; j < tiles && ok; ++j) {
         float4 x = make_float4(0.f, -INFINITY, 1.f, __int_as_float(-1));
@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (page >= 0) {
           const long long at = (long long)page * A.Hk + w.hk;
           const float vs = __ldg(A.v_scale + at);
-          x = make_float4(__ldg(A.k_scale + at), vs > 0.f ? log2f(vs) : 0.f,
-                          vs > 0.f ? 1.f / vs : -1.f, __int_as_float(page));
+          x = make_float4(__ldg(A.k_scale + at), vs > 0.f ? log2f(vs) : kNoScaleLog2,
+                          vs > 0.f ? 1.f / vs : -kNoScaleInverse, __int_as_float(page));
         }
         if (j >= kPageSlots)
           ok = all_wait(bar(M_PFREE + j % kPageSlots), (j / kPageSlots - 1) & 1, err);
