@@ -84,7 +84,8 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, int* err
   atomicExch(err, (int)MMDIT_ETIMEOUT);
   return false;
 }
-// The same by a whole warp that goes on together.
+// The same by a whole warp, which goes on or gives up together: where the lanes vote again
+// later, one that left alone would keep the others waiting for good.
 __device__ __forceinline__ bool all_wait(uint32_t bar, uint32_t parity, int* err) {
   return __all_sync(0xffffffffu, wait_for(bar, parity, err));
 }
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = j & 1;
       const uint32_t free = ((j >> 1) & 1) ^ 1;
       const bool more = j + 1 < tiles;
-      if (!(ok = wait_for(bar(M_KEMPTY + slot), free, err))) break;
+      if (!(ok = all_wait(bar(M_KEMPTY + slot), free, err))) break;
       store(smem + C::kKOff + slot * C::kTile, kr);
       fence_proxy_async_smem();
       mbar_arrive(bar(M_KFULL + slot));
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         next = find(j + 1);
         load(A.k, j + 1, kr);
       }
-      if (!ok || !(ok = wait_for(bar(M_VEMPTY + slot), free, err))) break;
+      if (!ok || !(ok = all_wait(bar(M_VEMPTY + slot), free, err))) break;
       if (scaled != 3) {  // no scale: zeros
 #pragma unroll
         for (int i = 0; i < NI; ++i)
