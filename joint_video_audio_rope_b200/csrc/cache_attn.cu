@@ -449,6 +449,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
   }
 
   // ---- the CTA's warps, merged in their order; the rings are done with
+  // set: an earlier kernel timed out, and attention kernels leave their outputs alone
+  const int skip = *(volatile int*)A.err;
   cp_async_wait<0>();
   __syncthreads();
   float(*sm_o)[kTile][D + 4] = reinterpret_cast<float(*)[kTile][D + 4]>(smem);
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
   constexpr int TPR = kFewWarps * 32 / kTile;  // threads per row
   constexpr int W = D / TPR;                   // channels per thread
   const int row = threadIdx.x / TPR, c0 = (threadIdx.x % TPR) * 4;
-  if (row >= live) return;
+  if (row >= live || skip != 0) return;
   float M = -INFINITY, L = 0.f, out[W];
 #pragma unroll
   for (int x = 0; x < kFewWarps; ++x) M = fmaxf(M, sm_ml[x][row][0]);
@@ -544,6 +546,7 @@ __global__ void __launch_bounds__(256)
   const bool live = b < A.B && tok < query_tokens(A, b);  // the same in all warps of a row
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
+  const int skip = *(volatile int*)A.err;  // set: the ranges have not been written
   const long long p0 = (long long)item * A.splits * tile + row;
   float M = -INFINITY, L = 0.f, out[W] = {};
   constexpr int kBatch = 8;  // ranges whose sums are under way at once, beside the maxima
@@ -594,6 +597,7 @@ __global__ void __launch_bounds__(256)
       for (int c = 0; c < W; ++c) out[c] += part[x][lane * W + c];
     }
   }
+  if (skip != 0) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
   T* dst = (T*)A.o + b * A.o_sb + (long long)tok * A.o_st + (long long)head * D + lane * W;
 #pragma unroll
