@@ -487,12 +487,14 @@ def rotary(q, q_out, q_desc, q_out_desc, k, k_out, k_desc, k_out_desc, layout: L
 
 
 def make_cache(k, v, k_scale, v_scale, page_table=None) -> Cache:
-    """Handle of a paged cache: codes [n_pages, heads, page_tokens, head_dim] of an 8-bit
-    dtype, scales float [n_pages, heads], page_table int32 [batch, max_pages] (None for calls that
-    take no tokens).  Holds addresses: keep the tensors alive."""
+    """Handle of a paged cache: e4m3 codes [n_pages, heads, page_tokens, head_dim] as
+    torch.float8_e4m3fn or as raw torch.uint8, scales float [n_pages, heads], page_table int32
+    [batch, max_pages] (None for calls that take no tokens).  Keeps the tensors alive."""
     import torch
-    if k.dim() != 4 or k.shape != v.shape or k.element_size() != 1 or v.element_size() != 1:
-        raise ValueError("expected 8-bit codes [n_pages, heads, page_tokens, head_dim] for k and v")
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    if k.dim() != 4 or k.shape != v.shape or k.dtype not in codes or v.dtype not in codes:
+        raise ValueError("expected e4m3 codes (float8_e4m3fn or uint8) [n_pages, heads, page_tokens, "
+                         "head_dim] for k and v")
     if any(x.shape != k.shape[:2] or x.dtype != torch.float32 for x in (k_scale, v_scale)):
         raise ValueError("expected float32 scales [n_pages, heads]")
     if not all(x.is_contiguous() for x in (k, v, k_scale, v_scale)):
