@@ -510,6 +510,7 @@ def make_cache(k, v, k_scale, v_scale, page_table=None) -> Cache:
     cache = Cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1],
                   k.shape[2], k.shape[3], _ptr(page_table), batch, per)
     cache.codes = k  # the device of the handle, for the calls' checks
+    cache.arrays = arrays  # alive while the handle is
     return cache
 
 

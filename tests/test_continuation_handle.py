@@ -27,3 +27,19 @@ def test_other_types_of_eight_bits_are_refused(dtype):
     for pair in ((bad[0], bad[1]), (good[0], bad[1]), (bad[0], good[1])):
         with pytest.raises(ValueError):
             M.make_cache(*pair, *good[2:])
+
+
+def test_a_handle_keeps_its_tensors_alive():
+    """A temporary (a clone, a .contiguous()) handed to make_cache would otherwise be freed, and its memory used for
+    something else, while the handle still holds the address."""
+    import gc
+    import weakref
+    x = _arrays()
+    refs = [weakref.ref(t) for t in x]
+    c = M.make_cache(*x)
+    del x
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del c
+    gc.collect()
+    assert all(r() is None for r in refs)
