@@ -498,7 +498,8 @@ enum { MMDIT_SCALE_NONE = 0, MMDIT_SCALE_LINEAR = 1, MMDIT_SCALE_NTK = 2, MMDIT_
  *           pairs that turn often over the trained extent keep their frequency,
  *           those that do not finish a turn are interpolated
  * where f_b = factor[b] > 0 and trained[b] > 0 are the extension factor and the
- * trained extent of the axis.  The turned pairs are multiplied by magnitude. */
+ * trained extent of the axis.  Parameters whose frequencies leave the range of a double
+ * (2^64 w_i is no number) are EINVAL.  The turned pairs are multiplied by magnitude. */
 typedef struct {
   double theta;
   int32_t dim_t, dim_h, dim_w;

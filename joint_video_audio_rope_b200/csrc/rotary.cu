@@ -245,6 +245,9 @@ int make_rotary_tab(const mmdit_rotary_params* r, int head_dim, RotaryTab& tab) 
         w = g * w + (1.0 - g) * w / f;
       }
       tab.half_turns[m] = w / pi;
+      // positions reach 2^63 (an audio token's numerator): their product is a number too
+      if (!isfinite(ldexp(tab.half_turns[m], 64)))
+        return fail(MMDIT_EINVAL, "rotary: frequency %g of pair %d of band %d is out of range", w, i, a);
     }
   }
   return MMDIT_OK;
