@@ -565,8 +565,9 @@ typedef struct {
  *   older tokens of the item it is at least the scale that is there (rounded up
  *   to a power of two); when it grows the older tokens' codes are rounded again.  Values become the nearest
  *   e4m3 value of x / s (ties to even).  A token with an infinity or NaN among
- *   its K or V values of a head keeps NaN codes for all of its K there, and zeros in
- *   place of such values of V: rows that attend to it give NaN, and no others.
+ *   its K or V values of a head, or whose K overflows fp32 when it is turned, keeps NaN
+ *   codes for all of its K there, and zeros in place of such values of V: rows that attend to
+ *   it give NaN, and no others.
  *   Every other slot of every page stays as it was.  Tokens at positions
  *   outside 0 .. capacity - 1, or whose page id is outside 0 .. n_pages - 1, are not
  *   stored.  No page may receive tokens at two places of the table in one call, and

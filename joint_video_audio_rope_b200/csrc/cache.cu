@@ -428,6 +428,19 @@ __global__ void __launch_bounds__(512, NV == 2 ? 2 : 1)
           for (int j = 0; j < NV * E; ++j)
             if (WHOLE || MODE == 2 || live(row0 + j / E * rstep))
               if (is_number(kx[j])) mk = abs_bits(kx[j], 0.f, mk);
+          // Turned values that overflowed mark their rows too.  Found from the raw rows again, pair
+          // m2 of each: a few instructions that run almost never, while rows found from kx cost the
+          // other path registers (480p clip, half pairs: 221 us instead of 166).
+          const int c1 = MODE == 2 ? ch1 : 2 * m2, c2 = MODE == 2 ? ch2 : 2 * m2 + 1;
+#pragma unroll 1
+          for (int row = prow0; row < page; row += pstep) {
+            if (!live(row)) continue;
+            const T* at = reinterpret_cast<const T*>(raw) + row * D;
+            const float x1 = (float)at[c1], x2 = (float)at[c2];
+            const float2 cs = angles[row * (D / 2) + angle_at];
+            if (!is_number(x1 * cs.x - x2 * cs.y) || !is_number(x1 * cs.y + x2 * cs.x))
+              atomicOr(&lost[row >> 5], 1u << (row & 31));
+          }
         }
         block_max(red[par]);
       }

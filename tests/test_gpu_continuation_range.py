@@ -53,3 +53,29 @@ def test_attention_beside_a_page_whose_v_scale_is_zero(M, kind, size, lead):
     host[3][:] = 2.0 ** size
     host[3][page] = 0.0
     _check_led(M, dtype, D, N, host, dev, cache, q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("half", [False, True])
+def test_append_of_keys_that_overflow_when_they_are_turned(M, dtype, half):
+    """Finite K whose turned value is beyond fp32: the token's K there is lost, as if it had held an infinity."""
+    rng = np.random.default_rng(55)
+    host, dev, cache = _new_cache(M, rng, 5, 3, 32, 64, 1, 3)
+    x = rng.standard_normal((1, 60, 3, 64))
+    big = 3.2e38  # its pairs' length is 4.5e38: some position turns a value beyond 3.4e38
+    for tok, h in ((7, 1), (40, 0), (41, 2)):
+        x[0, tok, h, :24] = big
+    (k, _), (v, _) = (_tensor(rng, x.shape, dtype, fill=a) for a in (x, rng.standard_normal(x.shape)))
+    mp, p = _params(M, (24, 20, 20), half, "none")
+    turned = OC.rotary(_f64(k), p, _olayout(_segments(M)), [0])
+    bad = (np.abs(turned) > 3.5e38).any(-1)
+    near = ((np.abs(turned) > 3.3e38).any(-1)) & ~bad
+    assert not near.any() and bad.any()
+    M.cache_append(k, v, M.desc_of(k), cache, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                   layout=M.make_layout(_segments(M)), rotation=mp)
+    OC.append(host[1], host[3], host[4], _f64(v), [0], [60], None)
+    assert np.array_equal(dev[1].cpu().numpy(), host[1]) and np.array_equal(dev[3].cpu().numpy(), host[3])
+    got = dev[0].cpu().numpy()
+    for i in range(60):
+        nan = got[host[4][0, i // 32], :, i % 32] & 127 == 127
+        assert np.array_equal(nan.all(-1), bad[0, i]) and not nan[~bad[0, i]].any()
