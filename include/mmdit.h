@@ -522,7 +522,7 @@ typedef struct {
  *   first  : NULL (0; the layout then holds at least N tokens) or device int32
  *            [B]: token n of item b has the position of the layout's token
  *            first[b] + n.  Indices outside the layout have position (0, 0, 0).
- *   Angles are fp64 until their whole turns are removed; products are fp32.
+ *   Angles, cosines and sines are fp64 and rounded to fp32 once; products are fp32.
  *   Errors : EINVAL, EUNSUPPORTED, ECUDA.
  */
 MMDIT_API int mmdit_rotary(const void* q, void* q_out, const mmdit_tensor_desc* q_desc,

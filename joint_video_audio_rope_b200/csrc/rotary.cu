@@ -214,7 +214,7 @@ int make_rotary_tab(const mmdit_rotary_params* r, int head_dim, RotaryTab& tab) 
   tab.ph = (dims[0] + dims[1]) / 2;
   tab.np = (int)sum / 2;
   tab.half = r->pairing == MMDIT_PAIR_HALF;
-  tab.magnitude = (float)r->magnitude;
+  tab.magnitude = r->magnitude;
   const double pi = 3.14159265358979323846;
   int m = 0;
   for (int a = 0; a < 3; ++a) {

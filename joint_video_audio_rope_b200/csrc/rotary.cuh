@@ -11,7 +11,7 @@ namespace mmdit {
 // band ends in pairs as in RopeTab, and how a pair's channels are found.
 struct RotaryTab {
   double half_turns[64];
-  float magnitude;
+  double magnitude;
   int pt, ph, np;  // pairs [0, pt) turn by t, [pt, ph) by h, [ph, np) by w
   int half;        // pair i of a band: (i, i + d_b / 2) instead of (2i, 2i + 1)
 };
@@ -46,16 +46,14 @@ __device__ __forceinline__ void token_position_f64(const DevLayout& L, long long
 
 // cos and sin (times the magnitude) of pair m at a position.  The angle of a
 // far position loses its fraction of a turn in fp32 (at position 10^6 its
-// rounding is 0.06 rad), so position x frequency and the removal of whole
-// turns are fp64; what is left, in [-1, 1] half turns, is rounded once.
+// rounding is 0.06 rad), so all of it is fp64, and cosine and sine are rounded once.
 __device__ __forceinline__ void rotary_cos_sin(const RotaryTab& tab, int m, double pt, double ph,
                                                double pw, float& c, float& s) {
   const double pos = m < tab.pt ? pt : (m < tab.ph ? ph : pw);
-  double a = pos * tab.half_turns[m];
-  a -= 2.0 * rint(0.5 * a);
-  sincospif((float)a, &s, &c);
-  c *= tab.magnitude;
-  s *= tab.magnitude;
+  double cd, sd;
+  sincospi(pos * tab.half_turns[m], &sd, &cd);
+  c = (float)(cd * tab.magnitude);
+  s = (float)(sd * tab.magnitude);
 }
 
 // The two channels of pair m (pairs from np on: the unturned channels).

@@ -79,3 +79,26 @@ def test_append_of_keys_that_overflow_when_they_are_turned(M, dtype, half):
     for i in range(60):
         nan = got[host[4][0, i // 32], :, i % 32] & 127 == 127
         assert np.array_equal(nan.all(-1), bad[0, i]) and not nan[~bad[0, i]].any()
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_rotary_products_are_all_that_rounds(M, half):
+    """Cosine and sine are rounded to fp32 once, 2^-24 of themselves, as are the first product and the result: with
+    |c|, |s| <= M, |err| <= 2^-24 |y| + 2^-24 M (|x1| + |x2|) + 2^-24 M |x2|."""
+    mp, p = _params(M, (40, 44, 44), half, "parts")
+    n = 20000
+    lay = M.make_layout([dict(kind=M.SEG_VIDEO, n_tokens=n, T=20, H=25, W=40, t0=10 ** 6)])
+    x = torch.randn((1, n, 1, 128), generator=torch.Generator(device="cuda").manual_seed(56), device="cuda")
+    y = torch.empty_like(x)
+    M.rotary(x, y, M.desc_of(x), M.desc_of(y), None, None, None, None, lay, mp)
+    j = torch.arange(n, device="cuda")
+    pos = torch.stack([10 ** 6 + j // 1000, j // 40 % 25, j % 40], 1).double()
+    xd, yd = x[0, :, 0].double(), y[0, :, 0].double()
+    for c1, c2, axis, w in OC.frequencies(p):
+        a = pos[:, axis] * w
+        c, s = torch.cos(a) * p["magnitude"], torch.sin(a) * p["magnitude"]
+        r1, r2 = xd[:, c1] * c - xd[:, c2] * s, xd[:, c1] * s + xd[:, c2] * c
+        room = 2.0 ** -24 * p["magnitude"] * (xd[:, c1].abs() + xd[:, c2].abs() + torch.maximum(xd[:, c1].abs(), xd[:, c2].abs()))
+        room = room * (1 + 2.0 ** -12)  # the oracle's angle: 2^-53 of 10^6 turns
+        assert bool(((yd[:, c1] - r1).abs() <= 2.0 ** -24 * r1.abs() + room).all())
+        assert bool(((yd[:, c2] - r2).abs() <= 2.0 ** -24 * r2.abs() + room).all())
