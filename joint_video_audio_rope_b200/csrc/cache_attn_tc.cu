@@ -15,9 +15,12 @@
 // With f = Q's factor^-1 * scale * log2(e) * (K scale), constant over the 16
 // tokens of a page group, the exponent is t = S f + log2(V scale): its row
 // maximum is found group by group from the maxima of S, so the scales cost eight
-// multiply-adds per row and tile.  P = 2^(t - m + 7) is held as fp16; m follows the
-// maximum only once it has grown by 2^8 (P <= 2^15 then), and terms down to 2^-32
-// of the largest are still held.  The sum of weights adds up 2^(t - m + 7) / (V scale) per
+// multiply-adds per row and tile.  P = 2^(t - m + 12) is held as fp16: rounded by 2^-11 down to
+// 2^-26 of the row's largest term and by 2^-37 of that below, so that the other tokens' terms
+// stay whole beside a leading token whose V is small; m follows the maximum only once it has
+// grown by 2^3 (P <= 2^15 then).  Three 480p frames: 2^7 and 2^8 took 0.2 to 1.1 % less time and kept terms
+// whole down to 2^-21 only, 2^14 and 2^1 (2^-28) took 0.7 to 1.9 % more.  The sum of weights adds up
+// 2^(t - m + 12) / (V scale) per
 // group.
 //
 // One B200: 4,680 rows x 24 heads over 37,440 tokens 1.58 ms at full clocks (1,304 TFLOP/s), 1.81 ms
@@ -36,8 +39,8 @@ constexpr int kKeys = 128;                // keys per tile
 constexpr int kHalf = 128 * 128;          // bytes of 64 channels of a 128-row fp16 tile
 constexpr int kThreads = 512;
 constexpr int kPageSlots = 8;             // tiles whose pages and scales are held
-constexpr float kManyShift = 7.f;         // P of a row's reference maximum: 2^7
-constexpr float kGrow = 8.f;              // the reference moves beyond 2^8
+constexpr float kManyShift = 12.f;        // P of a row's reference maximum: 2^12
+constexpr float kGrow = 3.f;              // the reference moves beyond 2^3 of it
 // registers per thread: softmax, converters, MMA warpgroup; 128 (2 a + b + c) = 65,536
 constexpr int kRegsSoftmax = 184, kRegsConvert = 104, kRegsMma = 40;
 static_assert(2 * kRegsSoftmax + kRegsConvert + kRegsMma <= 512, "register split");

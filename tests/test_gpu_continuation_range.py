@@ -102,3 +102,15 @@ def test_rotary_products_are_all_that_rounds(M, half):
         room = room * (1 + 2.0 ** -12)  # the oracle's angle: 2^-53 of 10^6 turns
         assert bool(((yd[:, c1] - r1).abs() <= 2.0 ** -24 * r1.abs() + room).all())
         assert bool(((yd[:, c2] - r2).abs() <= 2.0 ** -24 * r2.abs() + room).all())
+
+
+@pytest.mark.parametrize("kind", [k for k in KINDS if k[0] == "bf16"])
+def test_attention_past_a_leading_token_without_values(M, kind):
+    """The leading token's V codes are zeros, so the output is what the others add, exp(-lead) of the weight and less.
+    A weight is rounded to fp16 by 2^-11 of itself or 2^-39 of the row's largest, 2^-37 in the kernel of many rows: at 19
+    nats, 2^27.4, by 2^-11.6, at 17.5 nats, 2^25.2, by 2^-11.8."""
+    dtype, D, N = kind
+    host, dev, cache, q, (page, slot) = _led(M, np.random.default_rng(52), dtype, D, N, 19.0 if N <= 32 else 17.5)
+    host[1][page, :, slot] = 0
+    host[3][:] = 2.0 ** -6
+    _check_led(M, dtype, D, N, host, dev, cache, q)
