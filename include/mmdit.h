@@ -599,7 +599,8 @@ MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tenso
  *   none).  Scores, softmax statistics and sums are fp32.  The tensor cores' operands are
  *   fp16: codes as they are; q, each row brought to 2^14..2^15, rounded by 2^-11 of a value or
  *   2^-39 of the row's largest (so bf16 values stay exact down to 2^-29 of it); a token's weight times its V
- *   scale by 2^-11 of itself or 2^-37 of the row's largest.  fp32 calls take two such parts: 2^-22 or 2^-39.
+ *   scale by 2^-11 of itself or 2^-37 of the row's largest.  fp32 calls take two such parts: 2^-22 or 2^-39 for q, 2^-22
+ *   or 2^-51 for the weights.
  *   workspace : mmdit_cache_attn_workspace_size bytes (0 is possible), 256-byte
  *            aligned; partial results of split key ranges.  Two calls that may
  *            run at the same time need one each.

@@ -45,6 +45,10 @@ constexpr int kFewRows = 32;
 // behind the maximum by a factor of two (2^15 is still a number in fp16).
 constexpr float kShift = 14.f;
 constexpr float kGrow = 1.f;
+// fp32 calls: the second part of a probability is held times 2^12, which makes it as large as the
+// first one at most: held as it is, it was below fp16's numbers for what is 2^-27 of the
+// maximum, and two parts were no better than one.
+constexpr float kPartUp = 4096.f;
 
 __device__ __forceinline__ float2 unpack_half2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
@@ -390,8 +394,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
             pb[f][p][q][i] = transpose8(h);
             if (p + 1 < QP) {
               const float2 y = unpack_half2(h);
-              p0 -= y.x;
-              p1 -= y.y;
+              p0 = (p0 - y.x) * kPartUp;
+              p1 = (p1 - y.y) * kPartUp;
             }
           }
         }
@@ -427,19 +431,28 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int c = 0; c < 4; ++c) d[q][c] = kF32 ? 0.f : acc[q][j][c];
+      uint32_t a[HF][4];
 #pragma unroll
       for (int f = 0; f < HF; ++f) {
         // channels 2j and 2j + 1 of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
         const uint32_t pick = j & 1 ? 0x7362 : 0x5140;
         const uint32_t x = __byte_perm(vr[f][0][j >> 1], vr[f][1][j >> 1], pick);
         const uint32_t y = __byte_perm(vr[f][2][j >> 1], vr[f][3][j >> 1], pick);
-        uint32_t a[4];
-        halves_of(x, a[0], a[1]);
-        halves_of(y, a[2], a[3]);
+        halves_of(x, a[f][0], a[f][1]);
+        halves_of(y, a[f][2], a[f][3]);
+      }
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
+      for (int p = QP - 1; p >= 0; --p) {
 #pragma unroll
-          for (int p = QP - 1; p >= 0; --p) mma16816(d[q], a, pb[f][p][q][0], pb[f][p][q][1]);
+        for (int f = 0; f < HF; ++f)
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) mma16816(d[q], a[f], pb[f][p][q][0], pb[f][p][q][1]);
+        if (p > 0) {  // the small parts, back to size before the large ones join them
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) d[q][c] *= 1.f / kPartUp;
+        }
       }
 #pragma unroll
       for (int q = 0; q < NQ; ++q)

@@ -114,3 +114,30 @@ def test_attention_past_a_leading_token_without_values(M, kind):
     host[1][page, :, slot] = 0
     host[3][:] = 2.0 ** -6
     _check_led(M, dtype, D, N, host, dev, cache, q)
+
+
+@pytest.mark.parametrize("D,N", [(64, 3), (64, 12), (128, 5), (128, 20)])
+@pytest.mark.parametrize("lead", [12.0, 16.0, 20.0])
+def test_fp32_attention_past_a_leading_token_without_values(M, D, N, lead):
+    """The same in fp32, whose weights are two fp16 parts: each is whole to 2^-22 of itself down to 2^-29 (20 nats) of the
+    row's largest.  The scores are exact but for their rounding: K holds powers of two or zeros, Q a few bits, so that one
+    product of 12 to 20 nats and others of less than one are summed, each step truncated by 2^-23 of its sum: lead 2^-23 D / 16,
+    and with the exponent's own rounding (lead + 6) 2^-23; each moves a weight by its size, numerator and denominator alike."""
+    rng = np.random.default_rng(58)
+    host, dev, cache, q, (page, slot) = _led(M, rng, "f32", D, N, lead)
+    kc, vc, ks, vs, table = host
+    kc[:] = OC.to_e4m3(np.exp2(rng.integers(-3, 1, kc.shape)) * rng.choice([-1.0, 0.0, 1.0], kc.shape))
+    kc[..., 0] = 0
+    kc[page, 0, slot] = 0
+    kc[page, 0, slot, 0] = OC.to_e4m3(np.array(32.0))
+    vc[page, :, slot] = 0
+    vs[:] = 2.0 ** -6
+    x = np.round(rng.standard_normal((1, N, 1, D)) * 8) / 32
+    x[..., 0] = lead / 2  # times 32 times the scale, 2^-4
+    q.copy_(torch.from_numpy(x.astype(np.float32)))
+    for d, h in zip(dev, (kc, vc, ks.astype(np.float32), vs.astype(np.float32))):
+        d.copy_(torch.from_numpy(h))
+    got, _ = _attend(M, q, dev, cache, torch.tensor([150], dtype=torch.int32, device="cuda"), None, 0, 0.0625)
+    o, _, S, _ = OC.cache_attn(_f64(q), *host, [150], [N], 0, 0.0625)
+    w = 2.0 ** -22 + 2 * ((lead * D / 16 + 2 * (lead + 6)) * 2.0 ** -23) + (150 / 16 + 8) * 2.0 ** -23
+    assert np.all(np.abs(_f64(got) - o) <= 2.0 ** -24 * np.abs(o) + w * S)
