@@ -596,7 +596,8 @@ MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tenso
  *   A row that sees no token has o = 0 and lse = -inf.  Tokens on a page whose id
  *   is outside 0 .. n_pages - 1 are not seen.  Slots behind kv_len are never
  *   used, whatever they hold.  Codes of V may not be NaN (the append writes
- *   none).  Scores, softmax statistics and sums are fp32.  The tensor cores' operands are
+ *   none).  Scores, softmax statistics and sums are fp32; in
+ *   bf16 calls a running sum of the tensor cores, which truncate, takes in 2^17 tokens at most.  Their operands are
  *   fp16: codes as they are; q, each row brought to 2^14..2^15, rounded by 2^-11 of a value or
  *   2^-39 of the row's largest (so bf16 values stay exact down to 2^-29 of it); a token's weight times its V
  *   scale by 2^-11 of itself or 2^-37 of the row's largest.  fp32 calls take two such parts: 2^-22 or 2^-39 for q, 2^-22

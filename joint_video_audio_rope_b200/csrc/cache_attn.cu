@@ -40,6 +40,7 @@ constexpr int kFewWarps = 4;
 // bf16 rows per (item, K/V head) up to which tiles of 8 or 16 rows are taken: 24 heads over
 // 32,760 tokens, 32 rows: 78 us as two tiles, 84 on tcgen05; 48 rows: 105 and 85.
 constexpr int kFewRows = 32;
+constexpr long long kSummed = 1 << 17;  // most tokens in one running sum of a bf16 call
 // The probability of a row's reference maximum is held as 2^14: fp16 keeps its relative
 // precision down to 2^-14, so what is 2^-28 of it is still whole.  The reference may be
 // behind the maximum by a factor of two (2^15 is still a number in fp16).
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(256)
 struct CachePlan {
   int tile, tiles;  // rows per item, row tiles per (item, K/V head)
   long long items, whole;
-  int splits;
+  long long splits;
   size_t part_o_bytes, bytes;
   long long grid() const { return whole + (items - whole) * splits; }
 };
@@ -643,26 +644,31 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
   p.tile = q.dtype == MMDIT_BF16 && rows > kFewRows ? kManyTile : rows > 8 ? 16 : 8;
   p.tiles = (int)((rows + p.tile - 1) / p.tile);
   p.items = (long long)p.tiles * c.heads * q.batch;
+  // Ranges that one accumulator of the tensor cores sums: they truncate each sum, which over
+  // 2^20 tokens had lost 0.5 % of positive values.  (fp32 calls sum up slab by slab.)
+  const long long range = p.tile == kManyTile ? kSummed : q.dtype == MMDIT_BF16 ? kFewWarps * kSummed : cap;
+  const long long least = std::max(1LL, (cap + range - 1) / range);
   if (p.tile != kManyTile) {
     // A wave of as many CTAs as fit (Few::kCtas); a range is at least 256 tokens, two slabs per
     // warp, and a history of up to 512 is not split (3 rows x 8 heads over 20,000 tokens: 14.4 us
     // in ranges of 256, 16.1 of 512; over 1,000: 10.9 and 14.8).
     const int weight = q.head_dim * (p.tile / 8) * (q.dtype == MMDIT_F32 ? 2 : 1);
-    p.splits = (int)std::max(
-        1LL, std::min((weight > 256 ? 2 : 3) * 148 / p.items, cap <= 512 ? 1 : (cap + 255) / 256));
+    p.splits = std::max(
+        least, std::min((weight > 256 ? 2 : 3) * 148 / p.items, cap <= 512 ? 1 : (cap + 255) / 256));
     p.whole = p.splits > 1 ? 0 : p.items;
   } else {
     // One CTA per SM.  What is left behind the whole waves is split so that its
     // waves are short: ceil(left s / 148) waves of the key tiles of a range and about
     // three more for its set-up and its merge (100 rows x 24 heads over 1,024 tokens: 26 us
     // in one range, 19.5 in four).
-    p.whole = p.items / 148 * 148;
-    p.splits = 1;
+    p.whole = least > 1 ? 0 : p.items / 148 * 148;
+    p.splits = least;
     const long long left = p.items - p.whole, units = (cap + kUnit - 1) / kUnit;
+    const long long most = std::max(least, std::min(148LL, units / 2));
     long long best = 0;
-    for (int s = 1; s <= std::min(148LL, std::max(1LL, units / 2)); ++s) {
+    for (long long s = least; s <= most; ++s) {
       const long long cost = (left * s + 147) / 148 * ((units + s - 1) / s + (s > 1 ? 3 : 0));
-      if (s == 1 || cost < best) best = cost, p.splits = s;
+      if (s == least || cost < best) best = cost, p.splits = s;
     }
     if (p.splits == 1) p.whole = p.items;
   }
@@ -714,7 +720,8 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& A, const CachePlan& p, cudaSt
   return e;
 }
 
-int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c) {
+// checks q and the cache, and plans the call
+int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c, CachePlan& p) {
   int rc;
   if ((rc = check_cache_desc(q, "cache_attn q")) || (rc = check_cache(c, "cache_attn", true)))
     return rc;
@@ -725,6 +732,12 @@ int check_cache_attn(const mmdit_tensor_desc* q, const mmdit_cache* c) {
   const long long rows = (long long)q->n_tokens * (q->heads / c->heads) + kManyTile;
   if (rows > 0x7fffffffLL || (rows / 16 + 1) * c->heads * q->batch > 0x7fffffffLL)
     return fail(MMDIT_EINVAL, "cache_attn: too many query rows");
+  p = CachePlan{};
+  if (q->n_tokens == 0) return MMDIT_OK;
+  p = plan_cache_attn(*q, *c);
+  if (p.grid() > 0x7fffffffLL || (p.items - p.whole) * p.tile > 0x7ffffff0LL)  // CTAs, rows merged
+    return fail(MMDIT_EINVAL, "cache_attn: too many query rows over %lld tokens",
+                (long long)c->max_pages * c->page_tokens);
   return MMDIT_OK;
 }
 
@@ -737,8 +750,8 @@ using namespace mmdit;
 extern "C" {
 
 size_t mmdit_cache_attn_workspace_size(const mmdit_tensor_desc* q_desc, const mmdit_cache* cache) {
-  if (check_cache_attn(q_desc, cache) || q_desc->n_tokens == 0) return 0;
-  return plan_cache_attn(*q_desc, *cache).bytes;
+  CachePlan plan;
+  return check_cache_attn(q_desc, cache, plan) ? 0 : plan.bytes;
 }
 
 int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
@@ -747,7 +760,8 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
                      float* lse, void* workspace, size_t ws_bytes, mmdit_stream_t stream) {
   MMDIT_NVTX("mmdit_cache_attn");
   int rc;
-  if ((rc = check_cache_attn(q_desc, cache)) || (rc = check_cache_desc(o_desc, "cache_attn o")))
+  CachePlan plan;
+  if ((rc = check_cache_attn(q_desc, cache, plan)) || (rc = check_cache_desc(o_desc, "cache_attn o")))
     return rc;
   if (q_desc->batch != o_desc->batch || q_desc->n_tokens != o_desc->n_tokens ||
       q_desc->heads != o_desc->heads || q_desc->head_dim != o_desc->head_dim ||
@@ -760,7 +774,6 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   if (causal_block < 0) return fail(MMDIT_EINVAL, "cache_attn: causal_block %d", causal_block);
   if (!(scale > 0.f) || !isfinite(scale)) return fail(MMDIT_EINVAL, "cache_attn: scale must be > 0");
   if (q_desc->n_tokens == 0) return MMDIT_OK;
-  const CachePlan plan = plan_cache_attn(*q_desc, *cache);
   if (plan.bytes > 0) {
     if (workspace == nullptr || ws_bytes < plan.bytes)
       return fail(MMDIT_EWORKSPACE, "cache_attn: workspace needs %zu bytes", plan.bytes);
@@ -798,7 +811,7 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   A.scale_log2 = scale * 1.4426950408889634f;
   A.tiles = plan.tiles;
   A.whole = (int)plan.whole;
-  A.splits = plan.splits;
+  A.splits = (int)plan.splits;
   A.part_o = (float*)workspace;
   A.part_ml = (float*)((char*)workspace + plan.part_o_bytes);
   if ((A.err = device_error_flag()) == nullptr)

@@ -141,3 +141,26 @@ def test_fp32_attention_past_a_leading_token_without_values(M, D, N, lead):
     o, _, S, _ = OC.cache_attn(_f64(q), *host, [150], [N], 0, 0.0625)
     w = 2.0 ** -22 + 2 * ((lead * D / 16 + 2 * (lead + 6)) * 2.0 ** -23) + (150 / 16 + 8) * 2.0 ** -23
     assert np.all(np.abs(_f64(got) - o) <= 2.0 ** -24 * np.abs(o) + w * S)
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 200), ("bf16", 20), ("bf16", 1)])
+def test_the_running_sums_of_very_long_histories(M, dtype, rows):
+    """2^21 cached tokens, positive values, enough items that ranges are not split to fill the GPU.  A tensor core
+    truncates each of its sums by up to 2^-23; a running sum takes in 2^17 tokens at most, 2^13 steps of 16: 2^-10."""
+    B, D, page, kv = 300 if rows <= 32 else 148, 64, 128, 2 ** 21 - 5
+    per = 2 ** 21 // page
+    g = torch.Generator(device="cuda").manual_seed(53)
+    k = (torch.randn((per, 1, page, D), generator=g, device="cuda")).to(torch.float8_e4m3fn)
+    v = torch.randint(0x30, 0x38, (per, 1, page, D), generator=g, device="cuda", dtype=torch.uint8)  # 0.5 .. 0.94
+    ks, vs = (torch.ones((per, 1), device="cuda") for _ in range(2))
+    table = torch.arange(per, dtype=torch.int32, device="cuda").repeat(B, 1)
+    cache = M.make_cache(k.view(torch.uint8), v, ks, vs, table)
+    q = torch.randn((B, rows, 1, D), generator=g, device="cuda").to(torch.bfloat16)
+    o, lse = _attend(M, q, None, cache, torch.full((B,), kv, dtype=torch.int32, device="cuda"), None, 0, 0.125)
+    for b in (0, B - 1):
+        s = (q[b, :2, 0].double() @ k.reshape(-1, D)[:kv].double().T) * 0.125
+        w = torch.softmax(s, -1)
+        ref = sum(a @ x.double() for a, x in zip(w.split(2 ** 19, 1), v.view(torch.float8_e4m3fn).reshape(-1, D)[:kv].split(2 ** 19)))
+        err = (o[b, :2, 0].double() - ref).abs()
+        assert bool((err <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -11 + 2.0 ** -13) * ref).all()), float((err / ref).max())
+        assert float((lse[b, 0, :2].double() - torch.logsumexp(s, -1)).abs().max()) <= 2.0 ** -12
