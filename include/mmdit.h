@@ -539,7 +539,7 @@ MMDIT_API int mmdit_rotary(const void* q, void* q_out, const mmdit_tensor_desc* 
 typedef struct {
   void* k;                    /* codes, 16-byte aligned */
   void* v;
-  float* k_scale;             /* device float [n_pages, heads], each 0 or in 2^-60..2^60 */
+  float* k_scale;             /* device float [n_pages, heads], each 0 or in 2^-60..2^120 */
   float* v_scale;             /* (V scales of one item and head within 2^80 of one another,
                                  and up to 2^30 beside a scale of 0) */
   int32_t n_pages;
@@ -561,7 +561,7 @@ typedef struct {
  *   layout, rotary : both NULL, or K is turned (as by mmdit_rotary with first =
  *            start, in fp32, rounded only to its code) on the way in
  *   The scale of a (page, head) is the power of two s with max|x| / s in
- *   (224, 448] over the finite values stored in it, and >= 2^-60.  In a page that holds
+ *   (224, 448] over the finite values stored in it, and >= 2^-60 (2^120 at most, by fp32's range).  In a page that holds
  *   older tokens of the item it is at least the scale that is there (rounded up
  *   to a power of two); when it grows the older tokens' codes are rounded again.  Values become the nearest
  *   e4m3 value of x / s (ties to even).  A token with an infinity or NaN among

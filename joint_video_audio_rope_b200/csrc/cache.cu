@@ -92,7 +92,7 @@ struct AppendArgs {
   RotaryTab tab;
 };
 
-// The power of two s with amax / s in (224, 448], 2^-60 at least.
+// The power of two s with amax / s in (224, 448], 2^-60 at least (2^120 at most: amax < 2^128).
 __device__ __forceinline__ float fit_scale(float amax) {
   const int bits = __float_as_int(amax);
   int e = (bits >> 23) - 127 - 8;         // amax = m 2^(e + 8), m in [1, 2)

@@ -164,3 +164,25 @@ def test_the_running_sums_of_very_long_histories(M, dtype, rows):
         err = (o[b, :2, 0].double() - ref).abs()
         assert bool((err <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -11 + 2.0 ** -13) * ref).all()), float((err / ref).max())
         assert float((lse[b, 0, :2].double() - torch.logsumexp(s, -1)).abs().max()) <= 2.0 ** -12
+
+
+@pytest.mark.parametrize("kind", [("bf16", 64, 2), ("bf16", 64, 70), ("f32", 64, 2), ("f32", 64, 40), ("f32", 128, 2)])
+@pytest.mark.parametrize("size", [25, 37])
+def test_keys_and_values_beyond_the_small_scales(M, kind, size):
+    """K and V of 10^25 and 10^37, which the append stores with scales of 2^76 and 2^116, under a Q that brings the
+    scores back to ordinary ones."""
+    dtype, D, N = kind
+    rng = np.random.default_rng(54)
+    host, dev, cache = _new_cache(M, rng, 8, 2, 32, D, 1, 6)
+    k, _ = _tensor(rng, (1, 150, 2, D), dtype, fill=rng.standard_normal((1, 150, 2, D)) * 10.0 ** size)
+    v, _ = _tensor(rng, (1, 150, 2, D), dtype, fill=rng.standard_normal((1, 150, 2, D)) * 10.0 ** size)
+    M.cache_append(k, v, M.desc_of(k), cache, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    OC.append(host[0], host[2], host[4], _f64(k), [0], [150], np.zeros((1, 150, 2), bool))
+    OC.append(host[1], host[3], host[4], _f64(v), [0], [150], None)
+    for d, h in zip(dev[:4], host):
+        assert np.array_equal(d.cpu().numpy(), h)
+    x = rng.standard_normal((1, N, 2, D)) * 10.0 ** -size
+    q, _ = _tensor(rng, x.shape, dtype, fill=x)
+    got, lse = _attend(M, q, dev, cache, torch.tensor([150], dtype=torch.int32, device="cuda"), None, 0, 0.1)
+    ref = OC.cache_attn(_f64(q), *host, [150], [N], 0, 0.1)
+    _check_attention(dtype, D, 150, _f64(got), _f64(lse), ref, [N])
