@@ -480,7 +480,9 @@ MMDIT_API size_t mmdit_sparse_attn_table_workspace_size(const mmdit_tensor_desc*
  * frames and audio tokens that attend to everything generated before them).
  * The four calls below turn Q and K by their positions, keep K and V of the
  * past in pages of 8-bit codes, attend to them, and copy pages.  Tensors of
- * these calls are bf16 or f32 with head_dim 64 or 128, batch <= 65535.
+ * these calls are bf16 or f32 with head_dim 64 or 128, batch <= 65535.  Where
+ * n_tokens is 0 nothing is launched, and the tensors' addresses may be NULL (as those of
+ * an empty torch tensor are).
  */
 enum { MMDIT_PAIR_INTERLEAVED = 0, MMDIT_PAIR_HALF = 1 };
 enum { MMDIT_SCALE_NONE = 0, MMDIT_SCALE_LINEAR = 1, MMDIT_SCALE_NTK = 2, MMDIT_SCALE_PARTS = 3 };

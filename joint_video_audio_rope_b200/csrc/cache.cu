@@ -664,7 +664,9 @@ int mmdit_cache_append(const void* k, const void* v, const mmdit_tensor_desc* de
   if ((rc = check_cache_desc(desc, "cache_append")) ||
       (rc = check_cache(cache, "cache_append", true)))
     return rc;
-  if (!k || !v || !start) return fail(MMDIT_EINVAL, "cache_append: k, v and start must be non-NULL");
+  const bool some = desc->n_tokens > 0;  // tensors without tokens may have no address
+  if (!start || (some && (!k || !v)))
+    return fail(MMDIT_EINVAL, "cache_append: k, v and start must be non-NULL");
   if (!aligned16(k) || !aligned16(v))
     return fail(MMDIT_EINVAL, "cache_append: tensors must be 16-byte aligned");
   if (desc->batch != cache->batch || desc->heads != cache->heads ||

@@ -767,10 +767,12 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
       q_desc->heads != o_desc->heads || q_desc->head_dim != o_desc->head_dim ||
       q_desc->dtype != o_desc->dtype)
     return fail(MMDIT_EINVAL, "cache_attn: q and o descriptors disagree");
-  if (!q || !o || !kv_len) return fail(MMDIT_EINVAL, "cache_attn: q, o and kv_len must be non-NULL");
+  const bool some = q_desc->n_tokens > 0;  // tensors without tokens may have no address
+  if (!kv_len || (some && (!q || !o)))
+    return fail(MMDIT_EINVAL, "cache_attn: q, o and kv_len must be non-NULL");
   if (!aligned16(q) || !aligned16(o))
     return fail(MMDIT_EINVAL, "cache_attn: tensors must be 16-byte aligned");
-  if (o == q) return fail(MMDIT_EINVAL, "cache_attn: o aliases q");
+  if (some && o == q) return fail(MMDIT_EINVAL, "cache_attn: o aliases q");
   if (causal_block < 0) return fail(MMDIT_EINVAL, "cache_attn: causal_block %d", causal_block);
   if (!(scale > 0.f) || !isfinite(scale)) return fail(MMDIT_EINVAL, "cache_attn: scale must be > 0");
   if (q_desc->n_tokens == 0) return MMDIT_OK;

@@ -271,7 +271,17 @@ extern "C" int mmdit_rotary(const void* q, void* q_out, const mmdit_tensor_desc*
                             const mmdit_layout* layout, const mmdit_rotary_params* params,
                             const int32_t* first, int transpose, mmdit_stream_t stream) {
   MMDIT_NVTX("mmdit_rotary");
-  if (q == nullptr && k == nullptr) return fail(MMDIT_EINVAL, "rotary: q and k are both NULL");
+  if (q == nullptr && k == nullptr) {
+    // tensors without tokens may have no address; their descriptors tell
+    const mmdit_tensor_desc* d = q_desc != nullptr ? q_desc : k_desc;
+    if (d == nullptr || d->n_tokens != 0 || q_out != nullptr || k_out != nullptr)
+      return fail(MMDIT_EINVAL, "rotary: q and k are both NULL");
+    RotaryTab tab;
+    long long tokens;
+    if (const int rc = check_cache_desc(d, "rotary")) return rc;
+    if (const int rc = check_sequence(layout, "rotary", tokens)) return rc;
+    return make_rotary_tab(params, d->head_dim, tab);
+  }
   const void* in[2] = {q, k};
   void* out[2] = {q_out, k_out};
   const mmdit_tensor_desc* ind[2] = {q_desc, k_desc};
