@@ -593,7 +593,7 @@ MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tenso
  *            at position p = kv_len[b] - q_len[b] + i and sees tokens below
  *            (floor(p / c) + 1) c, i.e. its own block of c tokens (a frame; 1:
  *            itself) and the blocks before it; rows at p < 0 see nothing.
- *   scale  : > 0
+ *   scale  : > 0, below 2^127
  *   lse    : NULL or device float [B, heads, N]: natural-log sum of exp
  *   A row that sees no token has o = 0 and lse = -inf.  Tokens on a page whose id
  *   is outside 0 .. n_pages - 1 are not seen.  Slots behind kv_len are never

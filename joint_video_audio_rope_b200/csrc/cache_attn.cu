@@ -774,7 +774,9 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
     return fail(MMDIT_EINVAL, "cache_attn: tensors must be 16-byte aligned");
   if (some && o == q) return fail(MMDIT_EINVAL, "cache_attn: o aliases q");
   if (causal_block < 0) return fail(MMDIT_EINVAL, "cache_attn: causal_block %d", causal_block);
-  if (!(scale > 0.f) || !isfinite(scale)) return fail(MMDIT_EINVAL, "cache_attn: scale must be > 0");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !isfinite(scale_log2))
+    return fail(MMDIT_EINVAL, "cache_attn: scale must be > 0 and below 2^127");
   if (q_desc->n_tokens == 0) return MMDIT_OK;
   if (plan.bytes > 0) {
     if (workspace == nullptr || ws_bytes < plan.bytes)
@@ -810,7 +812,7 @@ int mmdit_cache_attn(const void* q, void* o, const mmdit_tensor_desc* q_desc,
   while ((1LL << A.g_shift) < A.G) ++A.g_shift;
   A.g_mul = (uint32_t)(((1ull << 32) * ((1ull << A.g_shift) - A.G)) / A.G + 1);
   A.causal = causal_block;
-  A.scale_log2 = scale * 1.4426950408889634f;
+  A.scale_log2 = scale_log2;
   A.tiles = plan.tiles;
   A.whole = (int)plan.whole;
   A.splits = (int)plan.splits;

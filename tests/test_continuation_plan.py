@@ -28,3 +28,9 @@ def test_calls_beyond_the_grid_are_refused():
     d = M.make_desc(65535, 2000, 1, 128, M.BF16)
     assert M.cache_attn_workspace_size(d, c) == 0
     assert _rc(M.cache_attn, 6 * FAKE, 7 * FAKE, d, d, c, FAKE, 0.1) == M.EINVAL
+
+
+@pytest.mark.parametrize("scale", [3e38, float("inf"), -1.0, float("nan"), 0.0])
+def test_scales_that_overflow_are_refused(scale):
+    d = M.make_desc(2, 40, 4, 128, M.BF16)
+    assert _rc(M.cache_attn, 6 * FAKE, 7 * FAKE, d, d, _cache(), FAKE, scale, workspace=FAKE * 16, ws_bytes=1 << 40) == M.EINVAL
