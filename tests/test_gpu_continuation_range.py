@@ -186,3 +186,58 @@ def test_keys_and_values_beyond_the_small_scales(M, kind, size):
     got, lse = _attend(M, q, dev, cache, torch.tensor([150], dtype=torch.int32, device="cuda"), None, 0, 0.1)
     ref = OC.cache_attn(_f64(q), *host, [150], [N], 0, 0.1)
     _check_attention(dtype, D, 150, _f64(got), _f64(lse), ref, [N])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_calls_allocate_no_device_memory(M, dtype):
+    """Nothing but the caller's arrays and workspace, in any form of the calls, once their kernels are loaded."""
+    rng = np.random.default_rng(59)
+    host, dev, cache = _new_cache(M, rng, 400, 2, 16, 64, 1, 300)
+    q = [_tensor(rng, (1, n, 4, 64), dtype)[0] for n in (1, 12, 100)]
+    k, _ = _tensor(rng, (1, 100, 2, 64), dtype)
+    o = [torch.empty_like(x) for x in q]
+    d = [M.desc_of(x) for x in q]
+    size = max(M.cache_attn_workspace_size(x, cache) for x in d)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    held = torch.tensor([4700], dtype=torch.int32, device="cuda")
+    start = torch.tensor([4600], dtype=torch.int32, device="cuda")
+    lay, free = M.make_layout(_segments(M)), sorted(set(range(400)) - set(host[4].ravel().tolist()))
+    kw = [dict()] + [dict(layout=lay, rotation=_params(M, (24, 20, 20), half, "none")[0]) for half in (False, True)]
+
+    def everything():
+        for x in kw:
+            M.cache_append(k, k, M.desc_of(k), cache, start, **x)
+        for x in kw[1:]:
+            M.rotary(q[2], o[2], d[2], d[2], None, None, None, None, lay, x["rotation"])
+        for x, y, z in zip(q, o, d):
+            M.cache_attn(x, y, z, z, cache, held, 0.125, causal_block=1, workspace=ws, ws_bytes=size)
+        M.cache_copy_pages(cache, [int(host[4][0, 0])], [free[0]])
+    everything()
+    torch.cuda.synchronize()
+    before = torch.cuda.mem_get_info()[0], torch.cuda.memory_stats()["allocation.all.allocated"]
+    for _ in range(3):
+        everything()
+    torch.cuda.synchronize()
+    assert (torch.cuda.mem_get_info()[0], torch.cuda.memory_stats()["allocation.all.allocated"]) == before
+
+
+@pytest.mark.parametrize("case", [  # D, page, B, N, H, Hk, per, kv, q_len, causal
+    (64, 32, 1, 300, 2, 2, 20, [600], None, 60), (128, 64, 2, 111, 6, 2, 9, [570, 111], [111, 40], 1),
+    (128, 16, 1, 257, 1, 1, 20, [310], None, 0)])
+def test_fp32_attention_of_many_rows(M, case):
+    D, page, B, N, H, Hk, per, kv, ql, causal = case
+    rng = np.random.default_rng(57)
+    host, dev, cache = _new_cache(M, rng, B * per + 2, Hk, page, D, B, per)
+    kc, vc, ks, vs, table = host
+    kc[kc & 127 == 127], vc[vc & 127 == 127] = 3, 3
+    vs[:] = np.exp2(rng.integers(-30, 10, vs.shape))
+    ks *= 2.0 ** -3
+    for d, h in zip(dev, (kc, vc, ks.astype(np.float32), vs.astype(np.float32))):
+        d.copy_(torch.from_numpy(h))
+    q, _ = _tensor(rng, (B, N, H, D), "f32", 4, 8)
+    kt = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    qt = None if ql is None else torch.tensor(ql, dtype=torch.int32, device="cuda")
+    got, lse = _attend(M, q, dev, cache, kt, qt, causal, 0.1)
+    ql = [N] * B if ql is None else ql
+    ref = OC.cache_attn(_f64(q), kc, vc, ks, vs, table, kv, ql, causal, 0.1)
+    _check_attention("f32", D, max(kv), _f64(got), _f64(lse), ref, ql)
