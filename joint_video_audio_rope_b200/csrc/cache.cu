@@ -16,7 +16,6 @@
 // One B200: 32,760 tokens x 24 heads of 128 in bf16 (604 MB, floor 92 us) 104 us as they are,
 // 122 us with interleaved rotation, 190 us with half pairs (whose partners meet no
 // alignment and cost single reads and writes of shared memory, and issue slots); 400 pages (315 MB, floor 48 us) 52 us.
-#include <cuda_fp16.h>
 #include <limits.h>
 
 #include <algorithm>
@@ -24,6 +23,7 @@
 #include <type_traits>
 #include <vector>
 
+#include "cache.cuh"
 #include "rotary.cuh"
 
 namespace mmdit {
@@ -106,9 +106,6 @@ __device__ __forceinline__ float floor_scale(float old) {
   const int bits = __float_as_int(old);
   return __int_as_float((bits + 0x7fffff) & 0x7f800000);
 }
-__device__ __forceinline__ float inverse_pow2(float s) {  // s = 2^e, e in -60..120
-  return __int_as_float((254 << 23) - __float_as_int(s));
-}
 __device__ __forceinline__ bool is_number(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 // Four values as e4m3 codes, to nearest, clipped to +-448; and the values of four codes.
@@ -124,12 +121,9 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 __device__ __forceinline__ void values4(uint32_t codes, float2& a, float2& b) {
   uint32_t lo, hi;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
-  a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  halves_of(codes, lo, hi);
+  a = unpack_half2(lo);
+  b = unpack_half2(hi);
 }
 
 // the values of one 16-byte vector
@@ -229,10 +223,6 @@ __device__ __forceinline__ void store_cluster(uint32_t to, int rank, float2 x) {
       "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(to),
       "r"(rank), "f"(x.x), "f"(x.y)
       : "memory");
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // MODE: 0 K as it is, 1 interleaved pairs, 2 half pairs.  A thread has NV 16-byte vectors

@@ -51,9 +51,6 @@ constexpr float kGrow = 1.f;
 // maximum, and two parts were no better than one.
 constexpr float kPartUp = 4096.f;
 
-__device__ __forceinline__ float2 unpack_half2(uint32_t h) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm(
@@ -76,9 +73,6 @@ __device__ __forceinline__ void load4(const T* p, float (&x)[4]) {
   }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }

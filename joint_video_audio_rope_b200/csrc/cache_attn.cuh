@@ -14,9 +14,7 @@
 // sum of weights and must not raise m, which would push the other terms out of fp16.
 #pragma once
 
-#include <cuda_fp16.h>
-
-#include "internal.h"
+#include "cache.cuh"
 
 namespace mmdit {
 
@@ -122,25 +120,13 @@ __device__ __forceinline__ float fit_half(float amax) {
   const int e = (__float_as_int(amax) >> 23) - 127;  // amax < 2^(e+1)
   return __int_as_float((min(max(14 - e, -126), 126) + 127) << 23);
 }
-// 1 / f of a power of two from 2^-126 to 2^126.
-__device__ __forceinline__ float inverse_pow2(float f) {
-  return __int_as_float((254 << 23) - __float_as_int(f));
-}
-// Four e4m3 codes as two pairs of fp16 (as one 32-bit register each: through the 16-bit
-// halves of the type's C++ interface this took three times the operations).
-__device__ __forceinline__ void halves_of(uint32_t codes, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
-}
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// 16 bytes to shared memory, asynchronously; zeros if not there.
+// cp_async16, or zeros if not there.
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(there ? 16 : 0)
