@@ -13,9 +13,10 @@
 // Copy.  The page lists travel in the kernel's parameters: no list has to be
 // copied to the device first, and one launch moves up to kCopyPairs pages.
 //
-// One B200: 32,760 tokens x 24 heads of 128 in bf16 (604 MB, floor 92 us) 104 us as they are,
-// 122 us with interleaved rotation, 190 us with half pairs (whose partners meet no
-// alignment and cost single reads and writes of shared memory, and issue slots); 400 pages (315 MB, floor 48 us) 52 us.
+// One B200: 32,760 tokens x 24 heads of 128 in bf16 (604 MB, floor 92 us) 107 us as they are,
+// 126 us with interleaved rotation, 163 us with half pairs (whose partners meet no
+// alignment and cost single reads and writes of shared memory, and issue slots); 15,600 fp32
+// tokens x 12 heads of 64 (120 MB, floor 18 us) 25, 31 and 36 us; 400 pages (315 MB, floor 48 us) 52 us.
 #include <limits.h>
 
 #include <algorithm>
@@ -529,7 +530,7 @@ cudaError_t launch_append_mode(AppendArgs& A, int batch, cudaStream_t s) {
   const int pages = (int)((A.N + page - 2LL) / page) + 1;  // most pages that N tokens touch
   // Slices of the heads, one CTA each: a CTA takes as long as its heads and about two
   // more for the page's look-ups and angles, and there are as many waves as the CTAs are of
-  // what fits (480p clip, bf16, interleaved: 122 us with one or two slices, 126 with four, 160 with
+  // what fits (480p clip, bf16, interleaved, side by side: 122 us with one or two slices, 126 with four, 160 with
   // eight; 1,560 tokens of it: 38, 23, 15 and 13).  Where K is turned, the CTAs of a page form
   // clusters of up to eight that share the work on its angles.
   const long long resident =

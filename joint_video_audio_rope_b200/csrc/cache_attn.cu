@@ -23,9 +23,11 @@
 // are the probabilities of an fp32 call.  Each warp runs its own softmax; the CTA's
 // warps, then the key ranges, are merged at the end in a fixed order.
 // One B200: 1 token of 24 heads over 75,600 tokens of 24 K/V heads (464 MB) 80 us = 5.8 TB/s, 0.89 of
-// the copy rate; of 8 K/V heads 34 us, 5 of them the merge; 11 fp32 rows over 2 x 32,760
-// tokens of 12 heads of 64 41 us, bound by issue slots (16 rows and two fp16 parts make about
-// 780 instructions per slab).
+// the copy rate; of 8 K/V heads 34 us, 4 to 5 of them the merge; 24 heads over 32,760 tokens (201 MB,
+// floor 31 us): 8 rows 41 us, 16 rows 49, 32 rows 77 (two tiles read the codes twice); 11 fp32
+// rows over 2 x 32,760 tokens of 12 heads of 64 41 us, bound by issue slots (16 rows and two fp16 parts
+// make about 780 instructions per slab), 218 fp32 rows over 32,760 tokens of 24 heads of 128 937 us: 14
+// tiles that read the codes one by one.
 #include <math.h>
 
 #include <algorithm>
@@ -38,7 +40,7 @@ namespace {
 
 constexpr int kFewWarps = 4;
 // bf16 rows per (item, K/V head) up to which tiles of 8 or 16 rows are taken: 24 heads over
-// 32,760 tokens, 32 rows: 78 us as two tiles, 84 on tcgen05; 48 rows: 105 and 85.
+// 32,760 tokens, 32 rows: 77 us as two tiles, 80 on tcgen05 (33 rows); 48 rows: 105 as three and 81.
 constexpr int kFewRows = 32;
 constexpr long long kSummed = 1 << 17;  // most tokens in one running sum of a bf16 call
 // The probability of a row's reference maximum is held as 2^14: fp16 keeps its relative
@@ -654,7 +656,7 @@ CachePlan plan_cache_attn(const mmdit_tensor_desc& q, const mmdit_cache& c) {
     // One CTA per SM.  What is left behind the whole waves is split so that its
     // waves are short: ceil(left s / 148) waves of the key tiles of a range and about
     // three more for its set-up and its merge (100 rows x 24 heads over 1,024 tokens: 26 us
-    // in one range, 19.5 in four).
+    // in one range when four took 19.5; they take 16.4 now).
     p.whole = least > 1 ? 0 : p.items / 148 * 148;
     p.splits = least;
     const long long left = p.items - p.whole, units = (cap + kUnit - 1) / kUnit;

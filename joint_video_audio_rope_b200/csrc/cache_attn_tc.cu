@@ -23,10 +23,13 @@
 // 2^(t - m + 12) / (V scale) per
 // group.
 //
-// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.58 ms at full clocks (1,304 TFLOP/s), 1.81 ms
-// under the power cap (1,138 TFLOP/s); 218 rows x 24 heads over 32,760 tokens 103 to 111 us. A row
-// tile's chain (scores out, softmax, P in, product) is what bounds it: 1.9 us per 128 keys with two tiles in turn, the
-// tensor pipe at 57 %, the exponentials at 58 % of their pipe, shared memory at 77 %.
+// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.85 ms in a running program (power cap, 1,116
+// TFLOP/s; the first calls 1.61 ms), head_dim 64 1.68 ms; 218 rows x 24 heads over 32,760 tokens 111 us, head_dim 64
+// 92; 100 rows over 1,024 tokens 16.4, over 128 10.3.  The tensor pipe is at 57 %, the exponentials at 58 % of
+// their pipe, shared memory at 79 %.  What bounds it, by clock stamps (three frames, 3,840 cycles per 128 keys
+// of two row tiles, 2,048 of them tensor work): a softmax warp computes for 2,600 and waits for its
+// scores for 1,240; the issuing warp waits for P for 1,770 and is in its issue code for 1,700, so
+// neither a row tile's chain (scores out, softmax, P in, product) nor the issue alone is all of it.
 #include <math.h>
 
 #include "cache_attn.cuh"
