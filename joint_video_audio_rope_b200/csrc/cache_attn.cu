@@ -319,12 +319,6 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       iv[f] = m4.y > 0.f ? __frcp_rn(m4.y) : 0.f;
       wv[f] = m4.y > 0.f ? iv[f] : kNoScaleInverse;
     }
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-#pragma unroll
-      for (int f = 0; f < HF; ++f)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[q][f][i] = fmaf(sc[q][f][i], mul[q][i & 1] * kf[f], lv[f]);
     if (__any_sync(0xffffffffu, n + S > full)) {
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
@@ -337,14 +331,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
     // ---- softmax of rows 2t (e = 0) and 2t + 1: the reference moves once a score is beyond
     // twice it, which few slabs need, so lanes seldom have to agree on a maximum
     bool grew = false;
-    float top[NQ][2];
+    float top[NQ][2], fac[NQ][HF][2];
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = sc[q][0][e];
+        float mx = -INFINITY;
 #pragma unroll
-        for (int f = 0; f < HF; ++f) mx = max3f(mx, sc[q][f][e], sc[q][f][2 + e]);
+        for (int f = 0; f < HF; ++f) {
+          // at least the smallest normal number: -inf stays -inf
+          fac[q][f][e] = fmaxf(mul[q][e] * kf[f], 1.1754944e-38f);
+          mx = fmaxf(mx, fmaf(fmaxf(sc[q][f][e], sc[q][f][2 + e]), fac[q][f][e], lv[f]));
+        }
         top[q][e] = mx;
         grew = grew || mx > m[q][e] + kGrow;
       }
@@ -381,8 +379,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // tokens g, then g + 8
-          float p0 = ex2_approx(sc[q][f][2 * i] - mref[q][0]);
-          float p1 = ex2_approx(sc[q][f][2 * i + 1] - mref[q][1]);
+          // one rounding, of what is left of the exponent beside the reference
+          float p0 = ex2_approx(fmaf(sc[q][f][2 * i], fac[q][f][0], lv[f] - mref[q][0]));
+          float p1 = ex2_approx(fmaf(sc[q][f][2 * i + 1], fac[q][f][1], lv[f] - mref[q][1]));
           l[q][0] = fmaf(p0, wv[f], l[q][0]);
           l[q][1] = fmaf(p1, wv[f], l[q][1]);
 #pragma unroll
@@ -535,8 +534,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, Few<T, D, NQ>::kCtas)
                      pack_bf16x2(out[c + 2] * inv, out[c + 3] * inv));
   }
   if (A.lse && threadIdx.x % TPR == 0)
-    A.lse[((long long)b * A.H + head) * A.N + tok] =
-        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    A.lse[((long long)b * A.H + head) * A.N + tok] = row_lse(M, L);
 }
 
 // Merges the key ranges of the split items in a fixed order: WPR warps per row (warp
@@ -618,8 +616,7 @@ __global__ void __launch_bounds__(256)
       *reinterpret_cast<uint32_t*>(dst + c) = pack_bf16x2(out[c] * inv, out[c + 1] * inv);
   }
   if (A.lse && lane == 0)
-    A.lse[((long long)b * A.H + head) * A.N + tok] =
-        L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    A.lse[((long long)b * A.H + head) * A.N + tok] = row_lse(M, L);
 }
 
 // Kernel, items, key ranges and workspace of a call, from what the host knows

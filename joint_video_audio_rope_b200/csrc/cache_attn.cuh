@@ -126,6 +126,17 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
+// Natural logarithm of a row's sum of exponentials from its reference (log2) and its sum, in
+// which V's scale left up to 60 octaves each, of opposite sign: the sum's exponent joins
+// the reference first, so that only the result is rounded.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  if (l == 0.f) return -INFINITY;
+  const int bits = __float_as_int(l);
+  if ((bits & 0x7f800000) == 0x7f800000) return l + m;  // no number
+  const float whole = m + (float)((bits >> 23) - 127);
+  return (whole + log2f(__int_as_float((bits & 0x7fffff) | 0x3f800000))) * 0.69314718055994531f;
+}
+
 // cp_async16, or zeros if not there.
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),

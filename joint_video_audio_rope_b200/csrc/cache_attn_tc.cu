@@ -593,8 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (A.lse && valid)
-            A.lse[((long long)w.b * A.H + head) * A.N + tok] =
-                l == 0.f ? -INFINITY : (mref + log2f(l)) * 0.69314718055994531f;
+            A.lse[((long long)w.b * A.H + head) * A.N + tok] = row_lse(mref, l);
         }
       }
     }

@@ -241,3 +241,24 @@ def test_fp32_attention_of_many_rows(M, case):
     ql = [N] * B if ql is None else ql
     ref = OC.cache_attn(_f64(q), kc, vc, ks, vs, table, kv, ql, causal, 0.1)
     _check_attention("f32", D, max(kv), _f64(got), _f64(lse), ref, ql)
+
+
+@pytest.mark.parametrize("D,N", [(64, 3), (64, 15), (128, 40)])
+@pytest.mark.parametrize("size", [-60, -45, -8, 30])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_fp32_sums_of_small_and_large_scales(M, D, N, size, zeros):
+    """A row's reference holds log2 of V's scale and its sum the scale's inverse: of the lse, where the two meet, only
+    the result may be rounded, and of an exponent only what the reference leaves of it.  With scores of almost 0: an
+    exponent of up to 16 rounds by 2^-21 (times ln 2), ex2 by 2^-22, eight sums and products by 2^-24 each, the logarithm and
+    its product by 2^-24 of the lse each."""
+    for kv in (17, 28, 40, 75, 160):
+        host, dev, cache, q, _ = _led(M, np.random.default_rng(60 + kv), "f32", D, N, 0.0, kv)
+        q.mul_(2.0 ** -7)
+        host[3][:] = 2.0 ** size
+        if zeros:
+            host[3][host[4][0, 1]] = 0.0
+        _check_led(M, "f32", D, N, host, dev, cache, q, kv)
+        _, lse = _attend(M, q, dev, cache, torch.tensor([kv], dtype=torch.int32, device="cuda"), None, 0, 0.0625)
+        _, want, _, A = OC.cache_attn(_f64(q), *host, [kv], [N], 0, 0.0625)
+        bound = 0.7 * 2.0 ** -21 + 2.0 ** -22 + 8 * 2.0 ** -24 + 2.0 ** -23 * np.abs(want) + (D / 16 + 2) * 2.0 ** -22 * A
+        assert np.all(np.abs(_f64(lse) - want) <= bound), float((np.abs(_f64(lse) - want) / bound).max())
