@@ -562,14 +562,14 @@ typedef struct {
  *   count  : NULL (N everywhere) or device int32 [B], clamped to 0..N
  *   layout, rotary : both NULL, or K is turned (as by mmdit_rotary with first =
  *            start, in fp32, rounded only to its code) on the way in
- *   The scale of a (page, head) is the power of two s with max|x| / s in
- *   (224, 448] over the finite values stored in it, and >= 2^-60 (2^120 at most, by fp32's range).  In a page that holds
- *   older tokens of the item it is at least the scale that is there (rounded up
- *   to a power of two); when it grows the older tokens' codes are rounded again.  Values become the nearest
- *   e4m3 value of x / s (ties to even).  A token with an infinity or NaN among
- *   its K or V values of a head, or whose K overflows fp32 when it is turned, keeps NaN
- *   codes for all of its K there, and zeros in place of such values of V: rows that attend to
- *   it give NaN, and no others.
+ *   The scale of a (page, head) is the power of two s with max|x| / s in (224, 448]
+ *   over the finite values stored in it, and >= 2^-60 (2^120 at most, by fp32's range).
+ *   In a page that holds older tokens of the item it is at least the scale that is
+ *   there (rounded up to a power of two); when it grows the older tokens' codes are
+ *   rounded again.  Values become the nearest e4m3 value of x / s (ties to even).  A
+ *   token with an infinity or NaN among its K or V values of a head, or whose K
+ *   overflows fp32 when it is turned, keeps NaN codes for all of its K there, and zeros
+ *   in place of such values of V: rows that attend to it give NaN, and no others.
  *   Every other slot of every page stays as it was.  Tokens at positions
  *   outside 0 .. capacity - 1, or whose page id is outside 0 .. n_pages - 1, are not
  *   stored.  No page may receive tokens at two places of the table in one call, and
@@ -595,15 +595,16 @@ MMDIT_API int mmdit_cache_append(const void* k, const void* v, const mmdit_tenso
  *            itself) and the blocks before it; rows at p < 0 see nothing.
  *   scale  : > 0, below 2^127
  *   lse    : NULL or device float [B, heads, N]: natural-log sum of exp
- *   A row that sees no token has o = 0 and lse = -inf.  Tokens on a page whose id
- *   is outside 0 .. n_pages - 1 are not seen.  Slots behind kv_len are never
- *   used, whatever they hold.  Codes of V may not be NaN (the append writes
- *   none).  Scores, softmax statistics and sums are fp32; in
- *   bf16 calls a running sum of the tensor cores, which truncate, takes in 2^17 tokens at most.  Their operands are
- *   fp16: codes as they are; q, each row brought to 2^14..2^15, rounded by 2^-11 of a value or
- *   2^-39 of the row's largest (so bf16 values stay exact down to 2^-29 of it); a token's weight times its V
- *   scale by 2^-11 of itself or 2^-37 of the row's largest.  fp32 calls take two such parts: 2^-22 or 2^-39 for q, 2^-22
- *   or 2^-51 for the weights.
+ *   A row that sees no token has o = 0 and lse = -inf.  Tokens on a page whose id is
+ *   outside 0 .. n_pages - 1 are not seen.  Slots behind kv_len are never used,
+ *   whatever they hold.  Codes of V may not be NaN (the append writes none).  Scores,
+ *   softmax statistics and sums are fp32; in bf16 calls a running sum of the tensor
+ *   cores, which truncate, takes in 2^17 tokens at most.  Their operands are fp16:
+ *   codes as they are; q, each row brought to 2^14..2^15, rounded by 2^-11 of a value
+ *   or 2^-39 of the row's largest (so bf16 values stay exact down to 2^-29 of it); a
+ *   token's weight times its V scale by 2^-11 of itself or 2^-37 of the row's largest.
+ *   fp32 calls take two such parts: 2^-22 or 2^-39 for q, 2^-22 or 2^-51 for the
+ *   weights.
  *   workspace : mmdit_cache_attn_workspace_size bytes (0 is possible), 256-byte
  *            aligned; partial results of split key ranges.  Two calls that may
  *            run at the same time need one each.

@@ -22,12 +22,13 @@
 // to 2^-29 of that; fp32 values are split into two fp16 parts (22 bits), and so
 // are the probabilities of an fp32 call.  Each warp runs its own softmax; the CTA's
 // warps, then the key ranges, are merged at the end in a fixed order.
-// One B200: 1 token of 24 heads over 75,600 tokens of 24 K/V heads (464 MB) 80 us = 5.8 TB/s, 0.89 of
-// the copy rate; of 8 K/V heads 34 us, 4 to 5 of them the merge; 24 heads over 32,760 tokens (201 MB,
-// floor 31 us): 8 rows 41 us, 16 rows 49, 32 rows 77 (two tiles read the codes twice); 11 fp32
-// rows over 2 x 32,760 tokens of 12 heads of 64 41 us, bound by issue slots (16 rows and two fp16 parts
-// make about 780 instructions per slab), 218 fp32 rows over 32,760 tokens of 24 heads of 128 937 us: 14
-// tiles that read the codes one by one.
+// One B200: 1 token of 24 heads over 75,600 tokens of 24 K/V heads (464 MB) 80 us = 5.8
+// TB/s, 0.89 of the copy rate; of 8 K/V heads 34 us, 4 to 5 of them the merge; 24 heads
+// over 32,760 tokens (201 MB, floor 31 us): 8 rows 41 us, 16 rows 49, 32 rows 77 (two tiles
+// read the codes twice); 11 fp32 rows over 2 x 32,760 tokens of 12 heads of 64 41 us, bound
+// by issue slots (16 rows and two fp16 parts make about 780 instructions per slab), 218
+// fp32 rows over 32,760 tokens of 24 heads of 128 937 us: 14 tiles that read the codes one
+// by one.
 #include <math.h>
 
 #include <algorithm>

@@ -10,26 +10,27 @@
 //   warp 13         looks up the pages and scales of the tiles to come
 // Tensor memory: [0,128) S0 / P0, [128,256) S1 / P1, then O0 and O1 (D columns each).
 //
-// S = Q K^T with Q as fp16: each row is multiplied by the power of two that puts
-// its largest value at 2^14..2^15 (bf16 is exact there down to 2^-29 of it).
-// With f = Q's factor^-1 * scale * log2(e) * (K scale), constant over the 16
-// tokens of a page group, the exponent is t = S f + log2(V scale): its row
-// maximum is found group by group from the maxima of S, so the scales cost eight
-// multiply-adds per row and tile.  P = 2^(t - m + 12) is held as fp16: rounded by 2^-11 down to
-// 2^-26 of the row's largest term and by 2^-37 of that below, so that the other tokens' terms
-// stay whole beside a leading token whose V is small; m follows the maximum only once it has
-// grown by 2^3 (P <= 2^15 then).  Three 480p frames: 2^7 and 2^8 took 0.2 to 1.1 % less time and kept terms
-// whole down to 2^-21 only, 2^14 and 2^1 (2^-28) took 0.7 to 1.9 % more.  The sum of weights adds up
-// 2^(t - m + 12) / (V scale) per
-// group.
+// S = Q K^T with Q as fp16: each row is multiplied by the power of two that puts its
+// largest value at 2^14..2^15 (bf16 is exact there down to 2^-29 of it). With f = Q's
+// factor^-1 * scale * log2(e) * (K scale), constant over the 16 tokens of a page group, the
+// exponent is t = S f + log2(V scale): its row maximum is found group by group from the
+// maxima of S, so the scales cost eight multiply-adds per row and tile.  P = 2^(t - m + 12)
+// is held as fp16: rounded by 2^-11 down to 2^-26 of the row's largest term and by 2^-37 of
+// that below, so that the other tokens' terms stay whole beside a leading token whose V is
+// small; m follows the maximum only once it has grown by 2^3 (P <= 2^15 then).  Three 480p
+// frames: 2^7 and 2^8 took 0.2 to 1.1 % less time and kept terms whole down to 2^-21 only,
+// 2^14 and 2^1 (2^-28) took 0.7 to 1.9 % more.  The sum of weights adds up 2^(t - m + 12) /
+// (V scale) per group.
 //
-// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.85 ms in a running program (power cap, 1,116
-// TFLOP/s; the first calls 1.61 ms), head_dim 64 1.68 ms; 218 rows x 24 heads over 32,760 tokens 111 us, head_dim 64
-// 92; 100 rows over 1,024 tokens 16.4, over 128 10.3.  The tensor pipe is at 57 %, the exponentials at 58 % of
-// their pipe, shared memory at 79 %.  What bounds it, by clock stamps (three frames, 3,840 cycles per 128 keys
-// of two row tiles, 2,048 of them tensor work): a softmax warp computes for 2,600 and waits for its
-// scores for 1,240; the issuing warp waits for P for 1,770 and is in its issue code for 1,700, so
-// neither a row tile's chain (scores out, softmax, P in, product) nor the issue alone is all of it.
+// One B200: 4,680 rows x 24 heads over 37,440 tokens 1.85 ms in a running program (power
+// cap, 1,116 TFLOP/s; the first calls 1.61 ms), head_dim 64 1.68 ms; 218 rows x 24 heads
+// over 32,760 tokens 111 us, head_dim 64 92; 100 rows over 1,024 tokens 16.4, over 128
+// 10.3.  The tensor pipe is at 57 %, the exponentials at 58 % of their pipe, shared memory
+// at 79 %.  What bounds it, by clock stamps (three frames, 3,840 cycles per 128 keys of two
+// row tiles, 2,048 of them tensor work): a softmax warp computes for 2,600 and waits for
+// its scores for 1,240; the issuing warp waits for P for 1,770 and is in its issue code for
+// 1,700, so neither a row tile's chain (scores out, softmax, P in, product) nor the issue
+// alone is all of it.
 #include <math.h>
 
 #include "cache_attn.cuh"

@@ -2,14 +2,14 @@
 // the head, frequencies scaled for longer sequences, any window of a sequence
 // per batch item, and the transposed rotation (the gradient of the rotation).
 //
-// Pair i of band b turns by pos_b * w_i (SkyReels-V4 digest novelties 4 and 5
-// for the positions):   y1 = M (x1 cos - x2 sin),  y2 = M (x1 sin + x2 cos),
-// with the sine's sign changed for the transpose.  One read and one write of
-// every channel: HBM bound.  As in rope.cu the angles depend on the token and
-// the pair only, so a thread finds its cosines and sines once and streams the
-// heads of Q and K past them.  One B200: a 480p layer (33,490 tokens, 24 + 24 heads of 128,
-// bf16, 823 MB) 139 us = 5.9 TB/s, 0.90 of the measured copy rate, fp32 259 us = 0.97; one token of eight
-// sequences 4.3 us, of which the look-ups, one fp64 angle and the round trip are all.
+// Pair i of band b turns by pos_b * w_i (SkyReels-V4 digest novelties 4 and 5 for the
+// positions):   y1 = M (x1 cos - x2 sin),  y2 = M (x1 sin + x2 cos), with the sine's sign
+// changed for the transpose.  One read and one write of every channel: HBM bound.  As in
+// rope.cu the angles depend on the token and the pair only, so a thread finds its cosines
+// and sines once and streams the heads of Q and K past them.  One B200: a 480p layer
+// (33,490 tokens, 24 + 24 heads of 128, bf16, 823 MB) 139 us = 5.9 TB/s, 0.90 of the
+// measured copy rate, fp32 259 us = 0.97; one token of eight sequences 4.3 us, of which the
+// look-ups, one fp64 angle and the round trip are all.
 //
 // Interleaved pairs sit inside a thread's 16-byte chunk.  Half pairs are d_b/2
 // channels apart, 22 and 21 channels for the bands of a 128-channel head, so
