@@ -247,7 +247,7 @@ int make_rotary_tab(const mmdit_rotary_params* r, int head_dim, RotaryTab& tab) 
       }
       tab.half_turns[m] = w / pi;
       // positions reach 2^63 (an audio token's numerator): their product is a number too
-      if (!isfinite(ldexp(tab.half_turns[m], 64)))
+      if (!(tab.half_turns[m] < 9e288))  // 2^-64 of the largest double
         return fail(MMDIT_EINVAL, "rotary: frequency %g of pair %d of band %d is out of range", w, i, a);
     }
   }
